@@ -24,7 +24,9 @@ STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED",
 # Every symbol include/moe.h declares (checked by the CPU test suite).
 EXPORTS = ("moe_workspace_size", "moe_route", "moe_dispatch", "moe_expert_ffn", "moe_combine", "moe_layer",
            "moe_layer_decode_noalloc", "moe_reset_status", "moe_get_status", "moe_launch_count",
-           "moe_set_wait_cycles", "moe_status_string")
+           "moe_set_wait_cycles", "moe_status_string", "moe_permute", "moe_permute_grad", "moe_unpermute",
+           "moe_unpermute_grad", "moe_mxfp_scale_stride", "moe_mxfp_quantize", "moe_mxfp_dequantize",
+           "moe_mxfp_matmul")
 
 
 class QMatrixC(ctypes.Structure):
@@ -73,6 +75,17 @@ def _load():
         "moe_launch_count": (ctypes.c_uint64, []),
         "moe_set_wait_cycles": (c_i64, [c_i64]),
         "moe_status_string": (ctypes.c_char_p, [c_i32]),
+        "moe_permute": (c_i32, [c_vp, c_i32, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp, c_sz, c_vp]),
+        "moe_permute_grad": (c_i32, [c_vp, c_i32, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp, c_sz, c_vp]),
+        "moe_unpermute": (c_i32, [c_vp, c_i32, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_sz, c_vp]),
+        "moe_unpermute_grad": (c_i32, [c_vp, c_vp, c_i32, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_sz,
+                                       c_vp]),
+        "moe_mxfp_scale_stride": (c_i32, [c_i32, c_i32]),
+        "moe_mxfp_quantize": (c_i32, [c_vp, c_i32, c_i64, c_i32, c_i32, ctypes.c_uint32, c_vp, c_vp, c_vp, c_vp,
+                                      c_vp]),
+        "moe_mxfp_dequantize": (c_i32, [c_vp, c_vp, c_i64, c_i32, c_i32, c_vp, c_vp, c_vp, c_i32, c_vp]),
+        "moe_mxfp_matmul": (c_i32, [c_vp, c_vp, c_vp, c_i32, c_i32, c_vp, c_vp, c_vp, c_i32, c_i32, c_vp, c_i32, c_vp,
+                                    c_i32, c_vp, c_sz, c_vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -274,3 +287,222 @@ def get_status(ws, stream=None) -> int:
     v = c_i32(0)
     _check("moe_get_status", LIB.moe_get_status(_ws(ws), _stream(stream), ctypes.byref(v)))
     return int(v.value)
+
+
+# ------------------------------------------------ operators around the step
+
+MOE_STATUS_BYTES = 8704
+FORMATS = {"mx": 1, "nv": 2}  # MOE_FP_MX, MOE_FP_NV
+_FP_BLOCK = {"mx": 32, "nv": 16}
+MOE_FP_SWIGLU = 1
+_DTYPES = {"bfloat16": 1, "float16": 2, "float32": 3, "uint8": 4}
+_dtype_codes = {}  # torch.dtype -> MOE_DT_*, filled on first use
+
+
+def new_status_workspace(device="cuda"):
+    """The smallest workspace: the status word of the calls below, cleared."""
+    import torch
+    return torch.zeros(MOE_STATUS_BYTES, dtype=torch.uint8, device=device)
+
+
+def _dtype(t, name, bytes_ok=False):
+    d = t.dtype
+    c = _dtype_codes.get(d)
+    if c is None:
+        c = _dtype_codes[d] = _DTYPES.get(str(d).replace("torch.", ""), 0)
+    if c == 0 or (c == 4 and not bytes_ok):
+        raise TypeError(f"{name}: dtype {d} where the call takes bf16, fp16 or fp32{' or uint8' if bytes_ok else ''}")
+    return c
+
+
+class _Call:
+    """The tensor arguments of one call: all on the current CUDA device (its
+    stream is the one the kernels run on), contiguous, of the expected type and
+    exactly the expected shape."""
+
+    __slots__ = ("device",)
+
+    def __init__(self):
+        if REQUIRE_CUDA:
+            import torch
+            self.device = torch.cuda.current_device()
+
+    def ptr(self, t, name, shape=None, dtype=None):
+        """Address of `t`; `dtype` is a MOE_DT_* code, or the name of a torch
+        dtype the header fixes."""
+        if t is None:
+            raise ValueError(f"{name}: required (the call takes no NULL here)")
+        if REQUIRE_CUDA and t.get_device() != self.device:
+            raise ValueError(f"{name}: must be a CUDA tensor on the current device {self.device}, got {t.device}")
+        if isinstance(dtype, int):
+            if _dtype(t, name, True) != dtype:
+                raise TypeError(f"{name}: dtype {t.dtype} differs from the call's other rows")
+        elif dtype is not None and _type_names(t) != dtype:
+            raise TypeError(f"{name}: dtype {t.dtype} where the call takes {dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: must be contiguous")
+        if shape is not None and t.shape != shape:
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+        return t.data_ptr()
+
+    def opt(self, t, name, shape, dtype):
+        return None if t is None else self.ptr(t, name, shape, dtype)
+
+    def count(self, t, name):
+        """A device int32 scalar (or one-element slice), or None."""
+        return None if t is None else self.ptr(t.reshape(-1), name, (1,), "int32")
+
+    def ws(self, t):
+        return self.ptr(t, "ws", None, "uint8"), t.numel()
+
+    def stream(self, stream):
+        if stream is None:
+            import torch
+            return torch.cuda.current_stream().cuda_stream
+        d = getattr(stream, "device", None)
+        if REQUIRE_CUDA and d is not None and d.index is not None and d.index != self.device:
+            raise ValueError(f"stream: on device {d.index}, the tensors are on {self.device}")
+        return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+_names = {}  # torch.dtype -> its name without "torch."
+
+
+def _type_names(t):
+    d = t.dtype
+    n = _names.get(d)
+    if n is None:
+        n = _names[d] = str(d).replace("torch.", "")
+    return n
+
+
+def _pairs(inv_perm, T):
+    """k of an inv_perm [T*k] (or [T, k])."""
+    n = inv_perm.numel()
+    if T == 0 or n % T or n == 0:
+        raise ValueError(f"inv_perm: {n} pairs for {T} tokens")
+    return n // T
+
+
+def permute(x, inv_perm, x_perm, ws, stream=None):
+    """moe_permute: x [T, H] to the rows x_perm [T*k, H] sorted by expert."""
+    c = _Call()
+    T, H = _shape2(x, "x")
+    if T == 0:
+        return
+    k, dt = _pairs(inv_perm, T), _dtype(x, "x", True)
+    w, n = c.ws(ws)
+    _check("moe_permute", LIB.moe_permute(c.ptr(x, "x"), dt, T, H, k, c.ptr(inv_perm, "inv_perm", None, "int32"),
+                                          c.ptr(x_perm, "x_perm", (T * k, H), dt), w, n, c.stream(stream)))
+
+
+def permute_grad(dx_perm, inv_perm, dx, ws, stream=None):
+    """moe_permute_grad: dx [T, H], the sum of each token's rows of dx_perm."""
+    c = _Call()
+    T, H = _shape2(dx, "dx")
+    if T == 0:
+        return
+    k, dt = _pairs(inv_perm, T), _dtype(dx, "dx")
+    w, n = c.ws(ws)
+    _check("moe_permute_grad", LIB.moe_permute_grad(c.ptr(dx_perm, "dx_perm", (T * k, H), dt), dt, T, H, k,
+                                                    c.ptr(inv_perm, "inv_perm", None, "int32"), c.ptr(dx, "dx"), w, n,
+                                                    c.stream(stream)))
+
+
+def unpermute(y_perm, inv_perm, topk_w, out, ws, stream=None):
+    """moe_unpermute: out [T, H], each token's rows weighted by topk_w [T, k]."""
+    c = _Call()
+    T, H = _shape2(out, "out")
+    if T == 0:
+        return
+    k, dt = _pairs(inv_perm, T), _dtype(out, "out")
+    w, n = c.ws(ws)
+    _check("moe_unpermute", LIB.moe_unpermute(c.ptr(y_perm, "y_perm", (T * k, H), dt), dt, T, H, k,
+                                              c.ptr(inv_perm, "inv_perm", None, "int32"),
+                                              c.ptr(topk_w, "topk_w", (T, k), "float32"), c.ptr(out, "out"), w, n,
+                                              c.stream(stream)))
+
+
+def unpermute_grad(dout, y_perm, inv_perm, topk_w, dy_perm, dtopk_w, ws, stream=None):
+    """moe_unpermute_grad: the gradients of y_perm and topk_w from dout [T, H]."""
+    c = _Call()
+    T, H = _shape2(dout, "dout")
+    if T == 0:
+        return
+    k, dt = _pairs(inv_perm, T), _dtype(dout, "dout")
+    w, n = c.ws(ws)
+    _check("moe_unpermute_grad",
+           LIB.moe_unpermute_grad(c.ptr(dout, "dout"), c.ptr(y_perm, "y_perm", (T * k, H), dt), dt, T, H, k,
+                                  c.ptr(inv_perm, "inv_perm", None, "int32"),
+                                  c.ptr(topk_w, "topk_w", (T, k), "float32"),
+                                  c.ptr(dy_perm, "dy_perm", (T * k, H), dt),
+                                  c.ptr(dtopk_w, "dtopk_w", (T, k), "float32"), w, n, c.stream(stream)))
+
+
+def _format(fmt):
+    f = FORMATS.get(fmt)
+    if f is None:
+        raise ValueError(f"format {fmt!r}: one of {', '.join(FORMATS)}")
+    return f
+
+
+def mxfp_scale_stride(cols, fmt) -> int:
+    """Scale bytes per row of a [*, cols] matrix in format "mx" or "nv"."""
+    s = int(LIB.moe_mxfp_scale_stride(cols, _format(fmt)))
+    if s == 0:
+        raise MoeError("moe_mxfp_scale_stride", 1)
+    return s
+
+
+def _stride(cols, fmt):  # moe_mxfp_scale_stride without a call
+    return (cols // _FP_BLOCK[fmt] + 15) // 16 * 16
+
+
+def mxfp_quantize(x, codes, scales, fmt, tensor_scale=None, swiglu=False, rows_dev=None, stream=None):
+    """moe_mxfp_quantize: x [rows, cols] (with swiglu: gate | up [rows, 2*cols])
+    to codes [rows, cols/2] and scales [rows, mxfp_scale_stride(cols, fmt)]."""
+    c, f = _Call(), _format(fmt)
+    rows, cols = _shape2(x, "x")
+    if swiglu:
+        if cols % 2:
+            raise ValueError(f"x: {cols} columns are no gate and up halves")
+        cols //= 2
+    _check("moe_mxfp_quantize",
+           LIB.moe_mxfp_quantize(c.ptr(x, "x"), _dtype(x, "x"), rows, cols, f, MOE_FP_SWIGLU if swiglu else 0,
+                                 c.opt(tensor_scale, "tensor_scale", (1,), "float32"), c.count(rows_dev, "rows_dev"),
+                                 c.ptr(codes, "codes", (rows, cols // 2), "uint8"),
+                                 c.ptr(scales, "scales", (rows, _stride(cols, fmt)), "uint8"), c.stream(stream)))
+
+
+def mxfp_dequantize(codes, scales, out, fmt, tensor_scale=None, rows_dev=None, stream=None):
+    """moe_mxfp_dequantize: the values of codes and scales into out [rows, cols]."""
+    c, f = _Call(), _format(fmt)
+    rows, cols = _shape2(out, "out")
+    _check("moe_mxfp_dequantize",
+           LIB.moe_mxfp_dequantize(c.ptr(codes, "codes", (rows, cols // 2), "uint8"),
+                                   c.ptr(scales, "scales", (rows, _stride(cols, fmt)), "uint8"), rows, cols, f,
+                                   c.opt(tensor_scale, "tensor_scale", (1,), "float32"),
+                                   c.count(rows_dev, "rows_dev"), c.ptr(out, "out"), _dtype(out, "out"),
+                                   c.stream(stream)))
+
+
+def mxfp_matmul(a_codes, a_scales, b_codes, b_scales, out, fmt, ws, offsets=None, a_tensor_scale=None,
+                b_tensor_scale=None, stream=None):
+    """moe_mxfp_matmul: rows a [R, K] times their expert's b [E, N, K] into out
+    [R, N]; offsets [E+1] as moe_dispatch writes them (None: E = 1)."""
+    c, f = _Call(), _format(fmt)
+    R, N = _shape2(out, "out")
+    if b_codes.dim() != 3:
+        raise ValueError(f"b_codes: shape {tuple(b_codes.shape)}, expected [E, N, K/2]")
+    E, _, half = b_codes.shape
+    S = _stride(2 * half, fmt)
+    w, n = c.ws(ws)
+    _check("moe_mxfp_matmul",
+           LIB.moe_mxfp_matmul(c.ptr(a_codes, "a_codes", (R, half), "uint8"),
+                               c.ptr(a_scales, "a_scales", (R, S), "uint8"),
+                               c.opt(a_tensor_scale, "a_tensor_scale", (1,), "float32"), R, 2 * half,
+                               c.ptr(b_codes, "b_codes", (E, N, half), "uint8"),
+                               c.ptr(b_scales, "b_scales", (E, N, S), "uint8"),
+                               c.opt(b_tensor_scale, "b_tensor_scale", (E,), "float32"), E, N,
+                               c.opt(offsets, "offsets", (E + 1,), "int32"), f, c.ptr(out, "out"),
+                               _dtype(out, "out"), w, n, c.stream(stream)))

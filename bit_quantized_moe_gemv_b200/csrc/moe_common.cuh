@@ -32,6 +32,7 @@ static_assert(sizeof(WsHeader) <= 256, "header must fit in 256 bytes");
 // moe_reset_status clears them with the header.
 constexpr size_t kDecodeCounterBytes = 8448;  // 65 expert slots x 128 bytes, rounded to 256
 constexpr size_t kWsResetBytes = 256 + kDecodeCounterBytes;
+static_assert(kWsResetBytes == MOE_STATUS_BYTES, "the smallest workspace is what moe_reset_status clears");
 
 // Offsets (bytes from the workspace base) of every workspace segment.
 struct WsLayout {

@@ -1,0 +1,352 @@
+// Rows sorted by expert and back, with their gradients:
+//   permute         xp[inv[t,j]] = x[t]
+//   permute_grad    dx[t]        = sum_j dxp[inv[t,j]]
+//   unpermute       out[t]       = sum_j w[t,j] y[inv[t,j]]
+//   unpermute_grad  dy[inv[t,j]] = w[t,j] dout[t],  dw[t,j] = <dout[t], y[inv[t,j]]>
+// inv is moe_dispatch's inv_perm; -1 is a pair without a row.
+//
+// All four are bound by HBM, and all four are driven by the token side of the
+// permutation: a token's row is read (or written) once whatever k is, a row no
+// pair points to is never touched, sums run over j in order in registers (no
+// atomics, the same bits every time) and are rounded once.
+#include "call_range.h"
+#include "op_util.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kWarps = 8;
+
+// Row of pair p, or -1. A row outside [0, nrows) is reported and left out.
+__device__ __forceinline__ int pair_row(const int* __restrict__ inv, long long p, long long nrows, WsHeader* hdr) {
+  const int r = inv[p];
+  if (r >= -1 && r < nrows) return r;
+  flag_error(hdr, MOE_ERR_DEVICE_FAULT, r);
+  return -1;
+}
+
+// A block has kWarps warps: `wpt` (a power of two) of them take consecutive
+// 32-vector segments of one token's row, so kWarps / wpt tokens per block;
+// gridDim.y blocks share the segments of long rows.
+struct TokenSplit {
+  int wpt;
+  int tokens() const { return kWarps / wpt; }
+  dim3 grid(int T, int nvec) const {
+    const int nseg = (nvec + 31) / 32;
+    int y = (nseg + wpt - 1) / wpt;
+    if (y > 65535) y = 65535;
+    return dim3(unsigned((T + tokens() - 1) / tokens()), unsigned(y));
+  }
+};
+TokenSplit token_split(int nvec) {
+  const int nseg = (nvec + 31) / 32;
+  int w = 1;
+  while (w < kWarps && w < nseg) w *= 2;
+  return {w};
+}
+
+// One warp: 32 vectors of a token's row are read once and written to the
+// token's k rows.
+template <typename V>
+__global__ void __launch_bounds__(kWarps * 32)
+permute_kernel(const V* __restrict__ x, const int* __restrict__ inv, int T, int k, int nvec, int wpt,
+               V* __restrict__ xp, WsHeader* hdr) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int t = blockIdx.x * (kWarps / wpt) + warp / wpt;
+  if (t >= T) return;
+  const long long p0 = (long long)t * k, nrows = (long long)T * k;
+  for (int s = blockIdx.y * wpt + warp % wpt; s < (nvec + 31) / 32; s += gridDim.y * wpt) {
+    const int c = s * 32 + lane;
+    V v{};
+    if (c < nvec) v = x[(size_t)t * nvec + c];
+    for (int j0 = 0; j0 < k; j0 += 32) {
+      const int mine = j0 + lane < k ? pair_row(inv, p0 + j0 + lane, nrows, hdr) : -1;
+      const int n = min(32, k - j0);
+      for (int j = 0; j < n; ++j) {
+        const int r = __shfl_sync(0xffffffffu, mine, j);
+        if (r >= 0 && c < nvec) xp[(size_t)r * nvec + c] = v;
+      }
+    }
+  }
+}
+
+// One warp: 32 vectors of out[t]; the rows of up to kBatch pairs are in
+// flight at a time.
+template <typename T, int N, bool kWeighted>
+__global__ void __launch_bounds__(kWarps * 32)
+unpermute_kernel(const Vec<T, N>* __restrict__ y, const int* __restrict__ inv, const float* __restrict__ w, int tokens,
+                 int k, int nvec, int wpt, Vec<T, N>* __restrict__ out, WsHeader* hdr) {
+  constexpr int kBatch = 8;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int t = blockIdx.x * (kWarps / wpt) + warp / wpt;
+  if (t >= tokens) return;
+  const long long p0 = (long long)t * k, nrows = (long long)tokens * k;
+  for (int s = blockIdx.y * wpt + warp % wpt; s < (nvec + 31) / 32; s += gridDim.y * wpt) {
+    const int c = s * 32 + lane;
+    float acc[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) acc[i] = 0.f;
+    for (int j0 = 0; j0 < k; j0 += 32) {
+      const bool has = j0 + lane < k;
+      const int mine = has ? pair_row(inv, p0 + j0 + lane, nrows, hdr) : -1;
+      float wmine = 1.f;
+      if (kWeighted && has) wmine = w[p0 + j0 + lane];
+      const int n = min(32, k - j0);
+      for (int j1 = 0; j1 < n; j1 += kBatch) {
+        Vec<T, N> v[kBatch];
+        int row[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          row[j] = __shfl_sync(0xffffffffu, mine, (j1 + j) & 31);
+          if (j1 + j >= n) row[j] = -1;
+          if (row[j] >= 0 && c < nvec) v[j] = y[(size_t)row[j] * nvec + c];
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          const float wj = kWeighted ? __shfl_sync(0xffffffffu, wmine, (j1 + j) & 31) : 1.f;
+          if (row[j] >= 0 && c < nvec) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+              acc[i] = kWeighted ? fmaf(wj, to_f32(v[j].v[i]), acc[i]) : acc[i] + to_f32(v[j].v[i]);
+          }
+        }
+      }
+    }
+    if (c < nvec) {
+      Vec<T, N> o;
+#pragma unroll
+      for (int i = 0; i < N; ++i) o.v[i] = from_f32<T>(acc[i]);
+      out[(size_t)t * nvec + c] = o;
+    }
+  }
+}
+
+// One pair per kPW warps: dy = w dout is written while <dout, y> is summed,
+// so y, dout and dy are each touched once per pair (dout comes from L1 or L2
+// for all but a token's first pair).
+template <typename T, int N, int kPW>
+__global__ void __launch_bounds__(kWarps * 32)
+unpermute_grad_kernel(const Vec<T, N>* __restrict__ dout, const Vec<T, N>* __restrict__ y,
+                      const int* __restrict__ inv, const float* __restrict__ w, long long pairs, int k, int nvec,
+                      Vec<T, N>* __restrict__ dy, float* __restrict__ dw, WsHeader* hdr) {
+  constexpr int kUnroll = kPW > 1 ? 1 : N * sizeof(T) == 16 ? 4 : 8;
+  __shared__ float part[kWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long p = (long long)blockIdx.x * (kWarps / kPW) + warp / kPW;
+  float sum = 0.f;
+  if (p < pairs) {
+    const int r = pair_row(inv, p, pairs, hdr);
+    if (r >= 0) {
+      const float wp = w[p];
+      const Vec<T, N>* d = dout + (size_t)(p / k) * nvec;
+      const Vec<T, N>* yr = y + (size_t)r * nvec;
+      Vec<T, N>* o = dy + (size_t)r * nvec;
+      for (int c0 = (warp % kPW) * 32 * kUnroll; c0 < nvec; c0 += kPW * 32 * kUnroll) {
+        Vec<T, N> a[kUnroll], b[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+          const int c = c0 + u * 32 + lane;
+          if (c < nvec) {
+            b[u] = yr[c];
+            a[u] = d[c];
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+          const int c = c0 + u * 32 + lane;
+          if (c < nvec) {
+            Vec<T, N> g;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+              const float x = to_f32(a[u].v[i]);
+              sum = fmaf(x, to_f32(b[u].v[i]), sum);
+              g.v[i] = from_f32<T>(wp * x);
+            }
+            o[c] = g;
+          }
+        }
+      }
+    }
+  }
+  sum = warp_sum(sum);
+  if (kPW == 1) {
+    if (lane == 0 && p < pairs) dw[p] = sum;
+  } else {
+    if (lane == 0) part[warp] = sum;
+    __syncthreads();
+    if (threadIdx.x == 0 && p < pairs) {
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) s += part[i];
+      dw[p] = s;
+    }
+  }
+}
+
+// Largest vector (bytes, at most 16) that the row size and every pointer allow.
+int vector_bytes(size_t row_bytes, const void* a, const void* b, const void* c, const void* d) {
+  const uintptr_t all = uintptr_t(row_bytes) | reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b) |
+                        reinterpret_cast<uintptr_t>(c) | reinterpret_cast<uintptr_t>(d);
+  return int(all & 15 ? all & (~all + 1) & 15 : 16);
+}
+
+cudaError_t done() {
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+template <typename V>
+cudaError_t run_permute(const void* x, const int* inv, int T, int k, size_t row_bytes, void* xp, WsHeader* hdr,
+                        cudaStream_t st) {
+  const int nvec = int(row_bytes / sizeof(V));
+  const TokenSplit s = token_split(nvec);
+  permute_kernel<V><<<s.grid(T, nvec), kWarps * 32, 0, st>>>(static_cast<const V*>(x), inv, T, k, nvec, s.wpt,
+                                                            static_cast<V*>(xp), hdr);
+  return done();
+}
+
+template <typename T, int N>
+cudaError_t run_unpermute(const void* y, const int* inv, const float* w, int tokens, int k, int H, void* out,
+                          WsHeader* hdr, cudaStream_t st) {
+  using V = Vec<T, N>;
+  const int nvec = H / N;
+  const TokenSplit s = token_split(nvec);
+  if (w)
+    unpermute_kernel<T, N, true><<<s.grid(tokens, nvec), kWarps * 32, 0, st>>>(
+        static_cast<const V*>(y), inv, w, tokens, k, nvec, s.wpt, static_cast<V*>(out), hdr);
+  else
+    unpermute_kernel<T, N, false><<<s.grid(tokens, nvec), kWarps * 32, 0, st>>>(
+        static_cast<const V*>(y), inv, nullptr, tokens, k, nvec, s.wpt, static_cast<V*>(out), hdr);
+  return done();
+}
+
+template <typename T, int N>
+cudaError_t run_unpermute_grad(const void* dout, const void* y, const int* inv, const float* w, int tokens, int k,
+                               int H, void* dy, float* dw, WsHeader* hdr, cudaStream_t st) {
+  using V = Vec<T, N>;
+  const long long pairs = (long long)tokens * k;
+  // few pairs: a block per pair, so that a row is read by eight warps at once
+  if (pairs < 1184)
+    unpermute_grad_kernel<T, N, kWarps><<<unsigned(pairs), kWarps * 32, 0, st>>>(
+        static_cast<const V*>(dout), static_cast<const V*>(y), inv, w, pairs, k, H / N, static_cast<V*>(dy), dw, hdr);
+  else
+    unpermute_grad_kernel<T, N, 1><<<unsigned((pairs + kWarps - 1) / kWarps), kWarps * 32, 0, st>>>(
+        static_cast<const V*>(dout), static_cast<const V*>(y), inv, w, pairs, k, H / N, static_cast<V*>(dy), dw, hdr);
+  return done();
+}
+
+// f<T, N> for the element type and the vector width that fits.
+#define MOE_DISPATCH_VEC(F, dtype, vb, ...)                                            \
+  do {                                                                                 \
+    if ((dtype) == MOE_DT_FP32) {                                                      \
+      if ((vb) == 16) return F<float, 4>(__VA_ARGS__);                                 \
+      if ((vb) == 8) return F<float, 2>(__VA_ARGS__);                                  \
+      return F<float, 1>(__VA_ARGS__);                                                 \
+    }                                                                                  \
+    if ((dtype) == MOE_DT_BF16) {                                                      \
+      if ((vb) == 16) return F<__nv_bfloat16, 8>(__VA_ARGS__);                         \
+      if ((vb) >= 4) return F<__nv_bfloat16, 2>(__VA_ARGS__);                          \
+      return F<__nv_bfloat16, 1>(__VA_ARGS__);                                         \
+    }                                                                                  \
+    if ((vb) == 16) return F<__half, 8>(__VA_ARGS__);                                  \
+    if ((vb) >= 4) return F<__half, 2>(__VA_ARGS__);                                   \
+    return F<__half, 1>(__VA_ARGS__);                                                  \
+  } while (0)
+
+cudaError_t launch_permute(const void* x, int size, int T, int H, int k, const int* inv, void* xp, WsHeader* hdr,
+                           cudaStream_t st) {
+  const size_t row = size_t(H) * size;
+  switch (vector_bytes(row, x, xp, nullptr, nullptr)) {
+    case 16: return run_permute<uint4>(x, inv, T, k, row, xp, hdr, st);
+    case 8: return run_permute<uint2>(x, inv, T, k, row, xp, hdr, st);
+    case 4: return run_permute<uint32_t>(x, inv, T, k, row, xp, hdr, st);
+    case 2: return run_permute<uint16_t>(x, inv, T, k, row, xp, hdr, st);
+    default: return run_permute<uint8_t>(x, inv, T, k, row, xp, hdr, st);
+  }
+}
+
+cudaError_t launch_unpermute(const void* y, int dtype, int T, int H, int k, const int* inv, const float* w, void* out,
+                             WsHeader* hdr, cudaStream_t st) {
+  const int vb = vector_bytes(size_t(H) * dtype_size(dtype), y, out, nullptr, nullptr);
+  MOE_DISPATCH_VEC(run_unpermute, dtype, vb, y, inv, w, T, k, H, out, hdr, st);
+}
+
+cudaError_t launch_unpermute_grad(const void* dout, const void* y, int dtype, int T, int H, int k, const int* inv,
+                                  const float* w, void* dy, float* dw, WsHeader* hdr, cudaStream_t st) {
+  const int vb = vector_bytes(size_t(H) * dtype_size(dtype), dout, y, dy, nullptr);
+  MOE_DISPATCH_VEC(run_unpermute_grad, dtype, vb, dout, y, inv, w, T, k, H, dy, dw, hdr, st);
+}
+
+// Shapes of the row operators: any H, the pair index in 32 bits.
+bool rows_shape_ok(int64_t T, int64_t H, int64_t k) {
+  return T >= 0 && H >= 1 && H <= (1 << 24) && k >= 1 && k <= kMaxK && T * k <= 0x7fffffffLL;
+}
+
+moe_status rows_check(const void* a, const void* b, int32_t dtype, bool bytes_ok, const void* inv, void* ws,
+                      size_t ws_bytes) {
+  const int size = dtype_size(dtype);
+  if (size == 0 || (size == 1 && !bytes_ok)) return MOE_ERR_UNSUPPORTED;
+  if (!a || !b || !inv || !ptr_aligned(a, size) || !ptr_aligned(b, size) || !ptr_aligned(inv, 4))
+    return MOE_ERR_INVALID_ARG;
+  return status_ws_check(ws, ws_bytes);
+}
+
+moe_status launched(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+moe_status moe_permute(const void* x, int32_t dtype, int32_t T, int32_t H, int32_t k, const int32_t* inv_perm,
+                       void* x_perm, void* ws, size_t ws_bytes, void* stream) {
+  const CallRange range("moe_permute");
+  if (!rows_shape_ok(T, H, k)) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  const moe_status s = rows_check(x, x_perm, dtype, true, inv_perm, ws, ws_bytes);
+  if (s != MOE_OK) return s;
+  return launched(launch_permute(x, dtype_size(dtype), T, H, k, inv_perm, x_perm, ws_at<WsHeader>(ws, 0),
+                                 static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_permute_grad(const void* dx_perm, int32_t dtype, int32_t T, int32_t H, int32_t k,
+                            const int32_t* inv_perm, void* dx, void* ws, size_t ws_bytes, void* stream) {
+  const CallRange range("moe_permute_grad");
+  if (!rows_shape_ok(T, H, k)) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  const moe_status s = rows_check(dx_perm, dx, dtype, false, inv_perm, ws, ws_bytes);
+  if (s != MOE_OK) return s;
+  return launched(launch_unpermute(dx_perm, dtype, T, H, k, inv_perm, nullptr, dx, ws_at<WsHeader>(ws, 0),
+                                   static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_unpermute(const void* y_perm, int32_t dtype, int32_t T, int32_t H, int32_t k, const int32_t* inv_perm,
+                         const float* topk_w, void* out, void* ws, size_t ws_bytes, void* stream) {
+  const CallRange range("moe_unpermute");
+  if (!rows_shape_ok(T, H, k)) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  const moe_status s = rows_check(y_perm, out, dtype, false, inv_perm, ws, ws_bytes);
+  if (s != MOE_OK) return s;
+  if (!topk_w || !ptr_aligned(topk_w, 4)) return MOE_ERR_INVALID_ARG;
+  return launched(launch_unpermute(y_perm, dtype, T, H, k, inv_perm, topk_w, out, ws_at<WsHeader>(ws, 0),
+                                   static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_unpermute_grad(const void* dout, const void* y_perm, int32_t dtype, int32_t T, int32_t H, int32_t k,
+                              const int32_t* inv_perm, const float* topk_w, void* dy_perm, float* dtopk_w, void* ws,
+                              size_t ws_bytes, void* stream) {
+  const CallRange range("moe_unpermute_grad");
+  if (!rows_shape_ok(T, H, k)) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  moe_status s = rows_check(dout, dy_perm, dtype, false, inv_perm, ws, ws_bytes);
+  if (s != MOE_OK) return s;
+  if (!y_perm || !ptr_aligned(y_perm, dtype_size(dtype)) || !topk_w || !ptr_aligned(topk_w, 4) || !dtopk_w ||
+      !ptr_aligned(dtopk_w, 4))
+    return MOE_ERR_INVALID_ARG;
+  return launched(launch_unpermute_grad(dout, y_perm, dtype, T, H, k, inv_perm, topk_w, dy_perm, dtopk_w,
+                                        ws_at<WsHeader>(ws, 0), static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

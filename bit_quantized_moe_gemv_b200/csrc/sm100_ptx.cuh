@@ -78,6 +78,35 @@ __device__ __forceinline__ void bulk_g2s(uint32_t dst, const void* src, uint32_t
                "l"(src), "r"(bytes), "r"(bar)
                : "memory");
 }
+// Tiled copies through a tensor map: the innermost coordinate times the
+// element size is a multiple of 16 bytes, out-of-range elements arrive as 0.
+__device__ __forceinline__ void tma_prefetch_map(const void* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
+          "r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+// Per-thread asynchronous copy of 4 bytes, of which `valid` (0..4) are read
+// and the rest arrive as 0.
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_t valid) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kPending>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
 __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
@@ -109,6 +138,36 @@ __device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64
       "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+
+// D[tmem] (+)= (A * scales) * (B * scales)^T on packed E2M1 operands, K = 64.
+// kind::mxf4: one E8M0 scale per 32 elements of K; kind::mxf4nvf4: one E4M3
+// scale per 16. sfa / sfb are the TMEM columns of the scale words: lane
+// (row % 32) of column (row / 32) holds 4 scale bytes of a row; the
+// instruction descriptor says which of them this K step takes.
+template <bool kNv>
+__device__ __forceinline__ void mma_fp4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                        uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  if constexpr (kNv)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::
+            "r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+
+// 32 rows x 16 bytes from shared memory into 4 TMEM columns, the same in each
+// of the four 32-lane quarters. Ordered before later MMAs of this thread.
+__device__ __forceinline__ void tmem_cp_32x128(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
 // Arrive (once) on an mbarrier when all prior tcgen05.mma of this thread complete.
@@ -158,6 +217,30 @@ __host__ __device__ __forceinline__ uint32_t idesc_bf16(int M, int N) {
          | (1u << 10)                   // B format bf16
          | (uint32_t(N >> 3) << 17)     // N / 8
          | (uint32_t(M >> 4) << 24);    // M / 16
+}
+
+// Shared-memory matrix descriptor without swizzle: 16-byte rows, 8-row groups
+// 128 bytes apart (the scale blocks tmem_cp_32x128 reads).
+__device__ __forceinline__ uint64_t smem_desc_rows16(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= uint64_t((saddr >> 4) & 0x3FFFu);
+  d |= uint64_t(128 >> 4) << 32;
+  d |= uint64_t(1) << 46;
+  return d;
+}
+
+// Instruction descriptor of the fp4 kinds: E2M1 A and B (K-major, packed),
+// fp32 D, M x N. `sf` picks the first of the scale bytes of a word (mxf4: 0
+// or 2; mxf4nvf4: 0).
+template <bool kNv>
+__host__ __device__ __forceinline__ uint32_t idesc_fp4(int M, int N, int sf) {
+  return (uint32_t(sf) << 4)            // B scale byte
+         | (1u << 7)                    // A format E2M1
+         | (1u << 10)                   // B format E2M1
+         | (uint32_t(N >> 3) << 17)     // N / 8
+         | (kNv ? 0u : (1u << 23))      // scale format: E4M3 or E8M0
+         | (uint32_t(M >> 7) << 27)     // M / 128
+         | (uint32_t(sf) << 29);        // A scale byte
 }
 
 }  // namespace ptx

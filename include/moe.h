@@ -257,6 +257,120 @@ moe_status moe_layer_decode_noalloc(const uint16_t* x, int32_t T, int32_t H, int
                                     int32_t* topk_idx, float* topk_w, float* logits_out, uint16_t* out,
                                     const moe_options* opts, void* stream);
 
+/*
+ * Operators around the step: rows sorted by expert and back, with their
+ * gradients, and microscaled 4-bit floating point. They need no scratch; the
+ * ones that take `ws` use only the status word at its start, so any workspace
+ * serves, or MOE_STATUS_BYTES bytes (256-byte aligned, cleared once with
+ * moe_reset_status). Calls that share such a `ws` may overlap, on one stream
+ * or several and inside captured graphs: they only ever set the status word.
+ * Inputs and outputs of a call must not overlap.
+ */
+#define MOE_STATUS_BYTES 8704
+
+/* Element types. */
+#define MOE_DT_BF16 1
+#define MOE_DT_FP16 2
+#define MOE_DT_FP32 3
+#define MOE_DT_U8 4
+
+/*
+ * moe_permute / moe_permute_grad - tokens to rows sorted by expert.
+ * moe_unpermute / moe_unpermute_grad - rows back to tokens, gates applied.
+ *   inv_perm   int32 [T*k] from moe_dispatch: the row of pair (t, j), or -1
+ *              for a pair that has none (an invalid expert id); an index
+ *              outside [-1, T*k) flags MOE_ERR_DEVICE_FAULT and counts as -1
+ *   permute:          x_perm[inv[t,j], :] = x[t, :]
+ *   permute_grad:     dx[t, :] = sum_j dx_perm[inv[t,j], :]
+ *   unpermute:        out[t, :] = sum_j topk_w[t,j] y_perm[inv[t,j], :]
+ *   unpermute_grad:   dy_perm[inv[t,j], :] = topk_w[t,j] dout[t, :]
+ *                     dtopk_w[t,j] = sum_h dout[t,h] y_perm[inv[t,j], h]
+ * x, dx, out, dout are [T, H], x_perm, dx_perm, y_perm, dy_perm [T*k, H], all
+ * of `dtype` (moe_permute takes MOE_DT_U8 as well: rows of packed codes or
+ * block scales); topk_w and dtopk_w are fp32 [T, k]. Any H in [1, 2^24],
+ * 1 <= k <= 64, T*k < 2^31; pointers aligned to their elements (16-byte
+ * aligned rows are fastest).
+ * Sums run in fp32, over j in order, and are rounded once; results do not
+ * depend on scheduling. Rows of x_perm and dy_perm that no pair points to are
+ * left as they were; a token without rows gets zeros, a pair without a row
+ * dtopk_w 0. A row is read even where its gate is 0.
+ */
+moe_status moe_permute(const void* x, int32_t dtype, int32_t T, int32_t H, int32_t k, const int32_t* inv_perm,
+                       void* x_perm, void* ws, size_t ws_bytes, void* stream);
+moe_status moe_permute_grad(const void* dx_perm, int32_t dtype, int32_t T, int32_t H, int32_t k,
+                            const int32_t* inv_perm, void* dx, void* ws, size_t ws_bytes, void* stream);
+moe_status moe_unpermute(const void* y_perm, int32_t dtype, int32_t T, int32_t H, int32_t k,
+                         const int32_t* inv_perm, const float* topk_w, void* out, void* ws, size_t ws_bytes,
+                         void* stream);
+moe_status moe_unpermute_grad(const void* dout, const void* y_perm, int32_t dtype, int32_t T, int32_t H, int32_t k,
+                              const int32_t* inv_perm, const float* topk_w, void* dy_perm, float* dtopk_w, void* ws,
+                              size_t ws_bytes, void* stream);
+
+/*
+ * Microscaled 4-bit floating point. A matrix [rows, cols] is held as
+ *   codes   uint8 [rows, cols/2]: element 2i in the low nibble of byte i, 2i+1
+ *           in the high one; E2M1: codes 0..7 are 0, 0.5, 1, 1.5, 2, 3, 4, 6,
+ *           bit 3 is the sign;
+ *   scales  uint8 [rows, S], S = moe_mxfp_scale_stride(cols, format): one byte
+ *           per block of consecutive elements of a row, then zeros up to a
+ *           multiple of 16 bytes (the product ignores what stands there);
+ * with
+ *   MOE_FP_MX  blocks of 32, scale byte b is E8M0: 2^(b-127), 255 = NaN;
+ *   MOE_FP_NV  blocks of 16, scale byte E4M3, and one fp32 scale per tensor
+ *              (NULL = 1) that multiplies all values; it must be a positive
+ *              normal number between 2^-90 and 2^90.
+ * cols is a multiple of 32, at most 2^24; codes, scales and the wide matrix are
+ * 16-byte aligned.
+ */
+#define MOE_FP_MX 1
+#define MOE_FP_NV 2
+
+/* Bytes between the scale rows of a [*, cols] matrix; 0 if cols or format is
+ * not supported. */
+int32_t moe_mxfp_scale_stride(int32_t cols, int32_t format);
+
+/*
+ * moe_mxfp_quantize - rows to codes and block scales.
+ *   x         bf16, fp16 or fp32 [rows, cols]; with MOE_FP_SWIGLU
+ *             [rows, 2*cols] = gate | up, and silu(gate) * up is quantised
+ *   rows_dev  NULL, or a DEVICE int32 (for example &offsets[E]): only the
+ *             first min(rows, max(0, *rows_dev)) rows are read and written
+ * MX: b - 127 = floor(log2(amax)) - 2, at least -127. NV: s = amax / (6 g)
+ * rounded to E4M3 (nearest even, at most 448). Elements: x over the scale,
+ * rounded to E2M1 (nearest even, at most 6), decided on the exact quotient. A
+ * block holding an infinity or a NaN (or whose silu(gate) * up leaves the
+ * fp32 range) gets a NaN scale and codes 0.
+ */
+#define MOE_FP_SWIGLU 1u
+moe_status moe_mxfp_quantize(const void* x, int32_t dtype, int64_t rows, int32_t cols, int32_t format,
+                             uint32_t flags, const float* tensor_scale, const int32_t* rows_dev, uint8_t* codes,
+                             uint8_t* scales, void* stream);
+
+/* moe_mxfp_dequantize - the values of codes and scales, rounded once to
+ * `dtype` (MX values are exact in bf16). rows_dev as above. */
+moe_status moe_mxfp_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int32_t cols,
+                               int32_t format, const float* tensor_scale, const int32_t* rows_dev, void* out,
+                               int32_t dtype, void* stream);
+
+/*
+ * moe_mxfp_matmul - grouped product of two microscaled matrices:
+ *   out[r, n] = ga gb[e] sum_k a[r, k] b[e, n, k]   for offsets[e] <= r < offsets[e+1]
+ *   a  [R, K], b  [E, N, K] in the same format (codes and scales as above)
+ *   a_tensor_scale  NULL or DEVICE fp32 [1]; b_tensor_scale NULL or [E] (NV)
+ *   offsets  int32 [E+1] as written by moe_dispatch, or NULL with E = 1: all
+ *            rows. Offsets that decrease or leave [0, R] flag
+ *            MOE_ERR_DEVICE_FAULT and nothing is written.
+ *   out      `out_dtype` (bf16, fp16, fp32) [R, N]; rows outside
+ *            [offsets[0], offsets[E]) are left as they were
+ * 0 <= R <= 2^30, 1 <= E <= 1024, 1 <= N <= 2^24, K a multiple of 32, N K < 2^41.
+ * Sums are fp32 on the fp4 tensor cores, rounded once. A NaN scale makes every
+ * result of its row (or of its weight row's column) NaN.
+ */
+moe_status moe_mxfp_matmul(const uint8_t* a_codes, const uint8_t* a_scales, const float* a_tensor_scale, int32_t R,
+                           int32_t K, const uint8_t* b_codes, const uint8_t* b_scales, const float* b_tensor_scale,
+                           int32_t E, int32_t N, const int32_t* offsets, int32_t format, void* out,
+                           int32_t out_dtype, void* ws, size_t ws_bytes, void* stream);
+
 /* Clear the device status word of a workspace (asynchronous on `stream`).
  * Call once on a fresh workspace before its first use. */
 moe_status moe_reset_status(void* ws, void* stream);
