@@ -7,18 +7,19 @@
 // the MMA (kind::mxf4 for MX, kind::mxf4nvf4 for NV); products are exact and
 // sums stay in fp32 in TMEM until the one rounding of the epilogue.
 //
-// One persistent CTA per SM, 12 warps:
-//   warp 0      codes: TMA tiles of 128 bytes (256 elements of K) per row,
-//               128-byte swizzle, kStages deep
-//   warp 1      MMA issuer (one thread): scale words smem -> TMEM
-//               (tcgen05.cp), then four K = 64 MMAs per stage
-//   warps 4-7   epilogue: TMEM -> registers -> smem (transposed) -> global,
-//               on the other of two accumulators
-//   warps 8-11  scales: 4-byte asynchronous copies that place each row's
-//               scale words in the blocked order tcgen05.cp wants
-// The scales come row-major, 4 bytes per row and K step apart by the row
-// stride, so no tiled copy can block them; per-thread copies can, and can mask
-// the bytes behind K.
+// One persistent CTA per SM, 16 warps:
+//   warp 0       codes: TMA tiles of 128 bytes (256 elements of K) per row,
+//                128-byte swizzle, kStages deep
+//   warp 1       MMA issuer, four K = 64 MMAs per stage
+//   warp 2       scales: TMA tiles of 32 bytes per row, kSlots deep
+//   warps 4-7    scale words from shared memory into TMEM, where the MMA reads
+//                them: lane (row % 32), column (row / 32), the same in all four
+//                lane quarters, so that each warp fills its own. They are
+//                written from registers because the rows' words are 4 bytes
+//                of a row-major matrix, which no copy into TMEM can gather; on
+//                the way the bytes behind K become 0
+//   warps 8-15   epilogue: TMEM -> registers -> smem (transposed) -> global,
+//                on the other of two accumulators
 //
 // Tiles: every CTA sums up the experts' token tiles (offsets are on the
 // device) in shared memory and takes tiles b, b + grid, ... of the list
@@ -39,34 +40,33 @@ namespace {
 constexpr int kBM = 128;       // weight rows per tile
 constexpr int kBKBytes = 128;  // code bytes of a row per stage: 256 elements
 constexpr int kBoxRows = 32;   // token rows per TMA box
-constexpr int kThreads = 384;
-constexpr int kEpiWarps = 4, kScaleWarps = 4;
+constexpr int kThreads = 512;
+constexpr int kEpiWarps = 8, kScaleWarps = 4;
+constexpr int kSlotRow = 32;   // scale bytes of a row per slot
+constexpr int kSlots = 3;
 constexpr int kScratch = 2048;  // epilogue staging per warp: 16 tokens x 32 rows x 4 bytes
 
 // kTN: tokens per tile (a multiple of 32); kStages: ring depth.
-template <bool kNv, int kTN, int kStages_>
+template <int kTN, int kStages>
 struct Cfg {
-  static constexpr int kStages = kStages_;
-  static constexpr int kWords = kNv ? 4 : 2;            // scale words per row and stage
-  static constexpr int kHalves = (kTN + 127) / 128;     // 128-row scale blocks of the token side
+  static constexpr int kBBlocks = (kTN + 31) / 32;  // 32-row blocks of the token side
   static constexpr int kABytes = kBM * kBKBytes;
-  static constexpr int kBBytes = kTN * kBKBytes;
-  static constexpr int kSfA = kABytes + kBBytes;        // offsets inside a stage
-  static constexpr int kSfB = kSfA + kWords * 512;
-  static constexpr int kStageBytes = (kSfB + kWords * kHalves * 512 + 1023) / 1024 * 1024;
-  static constexpr int kSfCols = kWords * 4 * (1 + kHalves);
-  // TMEM: two accumulators of kTN columns, then the scale words of kSfBufs stages
+  static constexpr int kStageBytes = kABytes + kTN * kBKBytes;
+  static constexpr int kSlotBytes = (kBM + kTN) * kSlotRow;
+  // TMEM: two accumulators of kTN columns, then buffers of the scale words of
+  // 16 bytes of each row: 4 x 4 columns of weights, 4 x kBCols of tokens
+  static constexpr int kBCols = (kBBlocks + 3) / 4 * 4;
+  static constexpr int kSfCols = 4 * (4 + kBCols);
   static constexpr int kSfBufs = (512 - 2 * kTN) / kSfCols >= 4 ? 4 : 2;
   static constexpr int kCols = 2 * kTN + kSfBufs * kSfCols;
   static constexpr int kTmemCols = kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
   static_assert(kCols <= 512, "TMEM");
-  static_assert(kStages > kSfBufs / 2 && kStages >= 3, "the scale loader runs kStages / 2 stages ahead");
-  static constexpr int kSmem = kStages * kStageBytes + kEpiWarps * kScratch + 1024;
+  static constexpr int kScaleAt = kStages * kStageBytes;  // offsets in shared memory
+  static constexpr int kScratchAt = kScaleAt + kSlots * kSlotBytes;
+  static constexpr int kSmem = kScratchAt + kEpiWarps * kScratch + 1024;
 };
 
 struct Args {
-  const uint8_t* a_scales;
-  const uint8_t* b_scales;
   const float* a_tscale;   // [1] or null
   const float* b_tscale;   // [E] or null
   const int* offsets;      // [E + 1] or null (one group of R rows)
@@ -76,6 +76,11 @@ struct Args {
   int vec_store;           // rows of out are 16-byte aligned
 };
 
+// Tensor maps: codes and scales of the weights and of the tokens.
+struct Maps {
+  CUtensorMap wcodes, tcodes, wscales, tscales;
+};
+
 struct Tile {
   int e, m0, row0, rows;
 };
@@ -83,15 +88,16 @@ struct Tile {
 // Token tiles of an expert with `rows` rows.
 __device__ __forceinline__ int token_tiles(int rows, int tn) { return (rows + tn - 1) / tn; }
 
-template <bool kNv, int kTN, int kStages_, typename OT>
+template <bool kNv, int kTN, int kStages, typename OT>
 __global__ void __launch_bounds__(kThreads, 1)
-fp4_gemm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap tmap, Args a) {
-  using C = Cfg<kNv, kTN, kStages_>;
-  constexpr int kStages = C::kStages;
+fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
+  using C = Cfg<kTN, kStages>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ __align__(8) uint64_t full_bar[kStages], scale_bar[kStages], empty_bar[kStages], accf_bar[2], acce_bar[2],
-      drain_bar;
+  __shared__ __align__(8) uint64_t full_bar[kStages], empty_bar[kStages];      // codes
+  __shared__ __align__(8) uint64_t sfull_bar[kSlots], sempty_bar[kSlots];      // scales in shared memory
+  __shared__ __align__(8) uint64_t wfull_bar[C::kSfBufs], wempty_bar[C::kSfBufs];  // scale words in TMEM
+  __shared__ __align__(8) uint64_t accf_bar[2], acce_bar[2], drain_bar;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh;
   __shared__ int off_sh[kMaxE + 1];    // first row of each expert
@@ -102,12 +108,21 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant_
   volatile int* abort_p = &abort_sh;
 
   if (threadIdx.x == 0) {
-    ptx::tma_prefetch_map(&wmap);
-    ptx::tma_prefetch_map(&tmap);
+    ptx::tma_prefetch_map(&maps.wcodes);
+    ptx::tma_prefetch_map(&maps.tcodes);
+    ptx::tma_prefetch_map(&maps.wscales);
+    ptx::tma_prefetch_map(&maps.tscales);
     for (int s = 0; s < kStages; ++s) {
       ptx::mbar_init(ptx::smem_addr(&full_bar[s]), 1);
-      ptx::mbar_init(ptx::smem_addr(&scale_bar[s]), kScaleWarps);
       ptx::mbar_init(ptx::smem_addr(&empty_bar[s]), 1);
+    }
+    for (int s = 0; s < kSlots; ++s) {
+      ptx::mbar_init(ptx::smem_addr(&sfull_bar[s]), 1);
+      ptx::mbar_init(ptx::smem_addr(&sempty_bar[s]), kScaleWarps);
+    }
+    for (int b = 0; b < C::kSfBufs; ++b) {
+      ptx::mbar_init(ptx::smem_addr(&wfull_bar[b]), kScaleWarps);
+      ptx::mbar_init(ptx::smem_addr(&wempty_bar[b]), 1);
     }
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(ptx::smem_addr(&accf_bar[b]), 1);
@@ -165,25 +180,25 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant_
   const uint32_t tmem = tmem_base_sh;
   const int MT = (a.N + kBM - 1) / kBM;
   const int KB = (a.K + 2 * kBKBytes - 1) / (2 * kBKBytes);
+  const int stride = scale_stride(kNv, a.K);
+  const int chunks = stride / 16;             // 16 scale bytes per row: one TMEM buffer
+  constexpr int kChunkStages = kNv ? 1 : 2;   // code stages they cover
   const long long ntiles = ok ? (long long)first_sh[a.E] * MT : 0;
 
+  // Called by whole warps: the last expert whose first tile is <= tt, by two
+  // rounds of 32 comparisons.
   auto tile_at = [&](long long t) {
     Tile r;
     const int tt = int(t / MT);
     r.m0 = int(t - (long long)tt * MT) * kBM;
-    int lo = 0, hi = a.E;  // the last expert whose first tile is <= tt
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (first_sh[mid] <= tt)
-        lo = mid;
-      else
-        hi = mid;
-    }
-    r.e = lo;
-    const int rows = off_sh[lo + 1] - off_sh[lo], nt = first_sh[lo + 1] - first_sh[lo], i = tt - first_sh[lo];
+    const int c = __popc(__ballot_sync(0xffffffffu, 32 * lane < a.E && first_sh[32 * lane] <= tt)) - 1;
+    const int e = 32 * c + lane;
+    r.e = 32 * c + __popc(__ballot_sync(0xffffffffu, e < a.E && first_sh[e] <= tt)) - 1;
+    const int lo = off_sh[r.e], rows = off_sh[r.e + 1] - lo;
+    const int nt = first_sh[r.e + 1] - first_sh[r.e], i = tt - first_sh[r.e];
     // tiles of one size, a multiple of 16 (at most kTN, so none is empty)
-    const int per = ((rows + nt - 1) / nt + 15) & ~15;
-    r.row0 = off_sh[lo] + i * per;
+    const int per = nt == 1 ? rows : ((rows + nt - 1) / nt + 15) & ~15;
+    r.row0 = lo + i * per;
     r.rows = min(per, rows - i * per);
     return r;
   };
@@ -198,158 +213,216 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant_
 
   if (warp == 0) {
     // ------------------------------------------------ codes
-    if (lane == 0) {
-      int s = 0, issued = 0;
-      uint32_t ph = 0;
-      for (long long t = blockIdx.x; t < ntiles && !*abort_p; t += gridDim.x) {
-        const Tile ti = tile_at(t);
-        const int boxes = (ti.rows + kBoxRows - 1) / kBoxRows;
-        const uint32_t bytes = uint32_t(C::kABytes + boxes * kBoxRows * kBKBytes);
-        for (int kb = 0; kb < KB; ++kb) {
-          if (!ptx::mbar_wait(ptx::smem_addr(&empty_bar[s]), ph ^ 1u, abort_p)) {
-            fail(7000001);
-            break;
-          }
-          const uint32_t bar = ptx::smem_addr(&full_bar[s]), dst = stage(s);
-          ptx::mbar_arrive_expect_tx(bar, bytes);
-          ptx::tma_load_3d(dst, &wmap, kb * kBKBytes, ti.m0, ti.e, bar);
-          for (int b = 0; b < boxes; ++b)
-            ptx::tma_load_2d(dst + C::kABytes + b * kBoxRows * kBKBytes, &tmap, kb * kBKBytes, ti.row0 + b * kBoxRows,
-                             bar);
-          issued = min(issued + 1, kStages);
-          if (++s == kStages) {
-            s = 0;
-            ph ^= 1u;
-          }
-        }
-      }
-      // no copy may be in flight when the CTA leaves
-      for (int i = 0; i < issued; ++i) {
-        if (--s < 0) {
-          s = kStages - 1;
-          ph ^= 1u;
-        }
-        ptx::mbar_wait(ptx::smem_addr(&full_bar[s]), ph, nullptr);
-      }
-    }
-  } else if (warp == 1) {
-    // ------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      int s = 0, it = 0;
-      uint32_t ph = 0;
-      long long n = 0;  // stages consumed
-      const uint32_t sf_base = tmem + 2 * kTN;
-      for (long long t = blockIdx.x; t < ntiles && !*abort_p; t += gridDim.x, ++it) {
-        const Tile ti = tile_at(t);
-        const int N = (ti.rows + 15) & ~15;
-        const int halves = N > 128 ? 2 : 1;
-        const int buf = it & 1;
-        if (!ptx::mbar_wait(ptx::smem_addr(&acce_bar[buf]), (uint32_t(it >> 1) & 1u) ^ 1u, abort_p)) {
-          fail(7000002);
-          break;
-        }
-        ptx::tc_fence_after();
-        const uint32_t d = tmem + uint32_t(buf * kTN);
-        bool good = true;
-        for (int kb = 0; kb < KB; ++kb, ++n) {
-          // the MMAs that read this scale buffer last are done: their stage was given back
-          if (n >= C::kSfBufs) {
-            const long long old = n - C::kSfBufs;
-            good = ptx::mbar_wait(ptx::smem_addr(&empty_bar[old % kStages]), uint32_t(old / kStages) & 1u, abort_p);
-          }
-          good = good && ptx::mbar_wait(ptx::smem_addr(&scale_bar[s]), ph, abort_p) &&
-                 ptx::mbar_wait(ptx::smem_addr(&full_bar[s]), ph, abort_p);
-          if (!good) {
-            fail(7000003);
-            break;
-          }
-          ptx::tc_fence_after();
-          const uint32_t base = stage(s);
-          const uint32_t sfa = sf_base + uint32_t(n % C::kSfBufs) * C::kSfCols, sfb = sfa + 4 * C::kWords;
-#pragma unroll
-          for (int w = 0; w < C::kWords; ++w) {
-            ptx::tmem_cp_32x128(sfa + 4 * w, ptx::smem_desc_rows16(base + C::kSfA + w * 512));
-            for (int h = 0; h < halves; ++h)
-              ptx::tmem_cp_32x128(sfb + 4 * (w * C::kHalves + h),
-                                  ptx::smem_desc_rows16(base + C::kSfB + (w * C::kHalves + h) * 512));
-          }
-          const int steps = min(4, (a.K - kb * 2 * kBKBytes + 63) / 64);
-          for (int ks = 0; ks < steps; ++ks) {
-            const int w = kNv ? ks : ks >> 1, sf = kNv ? 0 : 2 * (ks & 1);
-            ptx::mma_fp4<kNv>(d, ptx::smem_desc_k128(base + 32 * ks),
-                              ptx::smem_desc_k128(base + C::kABytes + 32 * ks), ptx::idesc_fp4<kNv>(kBM, N, sf),
-                              sfa + 4 * w, sfb + 4 * w * C::kHalves, (kb | ks) != 0);
-          }
-          ptx::mma_commit(ptx::smem_addr(&empty_bar[s]));
-          if (++s == kStages) {
-            s = 0;
-            ph ^= 1u;
-          }
-        }
-        if (!good) break;
-        ptx::mma_commit(ptx::smem_addr(&accf_bar[buf]));
-      }
-      ptx::mma_commit(ptx::smem_addr(&drain_bar));
-      ptx::mbar_wait(ptx::smem_addr(&drain_bar), 0, nullptr);
-    }
-  } else if (warp >= 8) {
-    // ------------------------------------------------ scales
-    constexpr int kAhead = kStages / 2;  // copies of this many stages are in flight per thread
-    constexpr int kRowsPer = 32 * kScaleWarps / C::kWords;
-    const int tid = threadIdx.x - 256;
-    const int word = tid % C::kWords, r0 = tid / C::kWords;
-    const int stride = scale_stride(kNv, a.K), blocks = a.K / (kNv ? 16 : 32);
-    int s = 0, pending = 0, sd = 0;  // stage to fill, stages in flight, next stage to hand over
+    int s = 0, issued = 0;
     uint32_t ph = 0;
-    auto hand_over = [&]() {
-      ptx::fence_proxy_async_smem();  // written by this thread, read by the tensor core's copies
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&scale_bar[sd]));
-      sd = sd + 1 == kStages ? 0 : sd + 1;
-      --pending;
-    };
     for (long long t = blockIdx.x; t < ntiles && all_ok(!*abort_p); t += gridDim.x) {
       const Tile ti = tile_at(t);
-      const uint8_t* wsrc = a.b_scales + ((size_t)ti.e * a.N + ti.m0) * stride;
-      const uint8_t* tsrc = a.a_scales + (size_t)ti.row0 * stride;
-      const int wrows = min(kBM, a.N - ti.m0);
-      const int tpad = (ti.rows + 15) & ~15;
+      const int boxes = (ti.rows + kBoxRows - 1) / kBoxRows;
+      const uint32_t bytes = uint32_t(C::kABytes + boxes * kBoxRows * kBKBytes);
       for (int kb = 0; kb < KB; ++kb) {
         if (!all_ok(ptx::mbar_wait(ptx::smem_addr(&empty_bar[s]), ph ^ 1u, abort_p))) {
-          fail(7000004);
+          fail(7000001);
           break;
         }
-        const int at = (kb * C::kWords + word) * 4;
-        const uint32_t left = uint32_t(max(0, min(4, blocks - at)));  // bytes of this word inside K
-        const uint32_t dst = stage(s) + C::kSfA + word * 512;
-#pragma unroll
-        for (int r = r0; r < kBM; r += kRowsPer) {
-          const uint32_t valid = r < wrows ? left : 0;
-          ptx::cp_async4(dst + (r & 31) * 16 + (r >> 5) * 4, valid ? wsrc + (size_t)r * stride + at : wsrc, valid);
+        if (ptx::elect_one()) {
+          const uint32_t bar = ptx::smem_addr(&full_bar[s]), dst = stage(s);
+          ptx::mbar_arrive_expect_tx(bar, bytes);
+          ptx::tma_load_3d(dst, &maps.wcodes, kb * kBKBytes, ti.m0, ti.e, bar);
+          for (int b = 0; b < boxes; ++b)
+            ptx::tma_load_2d(dst + C::kABytes + b * kBoxRows * kBKBytes, &maps.tcodes, kb * kBKBytes,
+                             ti.row0 + b * kBoxRows, bar);
         }
-        const uint32_t dstb = stage(s) + C::kSfB + word * C::kHalves * 512;
-        for (int r = r0; r < tpad; r += kRowsPer) {
-          const uint32_t valid = r < ti.rows ? left : 0;
-          ptx::cp_async4(dstb + (r >> 7) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4,
-                         valid ? tsrc + (size_t)r * stride + at : tsrc, valid);
-        }
-        ptx::cp_async_commit();
-        if (++pending > kAhead) {
-          ptx::cp_async_wait<kAhead>();
-          hand_over();
-        }
+        __syncwarp();
+        issued = min(issued + 1, kStages);
         if (++s == kStages) {
           s = 0;
           ph ^= 1u;
         }
       }
     }
-    ptx::cp_async_wait<0>();
-    while (pending > 0) hand_over();
-  } else if (warp >= 4) {
+    // no copy may be in flight when the CTA leaves
+    for (int i = 0; i < issued; ++i) {
+      if (--s < 0) {
+        s = kStages - 1;
+        ph ^= 1u;
+      }
+      ptx::mbar_wait(ptx::smem_addr(&full_bar[s]), ph, nullptr);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------ MMA issuer
+    int s = 0, it = 0;
+    uint32_t ph = 0;
+    int wb = 0;  // scale buffer
+    uint32_t wph = 0;
+    const uint32_t sf_base = tmem + 2 * kTN;
+    for (long long t = blockIdx.x; t < ntiles && all_ok(!*abort_p); t += gridDim.x, ++it) {
+      const Tile ti = tile_at(t);
+      const int N = (ti.rows + 15) & ~15;
+      const int buf = it & 1;
+      if (!all_ok(ptx::mbar_wait(ptx::smem_addr(&acce_bar[buf]), (uint32_t(it >> 1) & 1u) ^ 1u, abort_p))) {
+        fail(7000002);
+        break;
+      }
+      const uint32_t d = tmem + uint32_t(buf * kTN);
+      const uint32_t idesc = ptx::idesc_fp4<kNv>(kBM, N, 0), idesc2 = ptx::idesc_fp4<kNv>(kBM, N, kNv ? 0 : 2);
+      bool good = true;
+      for (int kb = 0; kb < KB; ++kb) {
+        const bool first = kb % kChunkStages == 0, last = kb % kChunkStages == kChunkStages - 1 || kb + 1 == KB;
+        if (first) good = ptx::mbar_wait(ptx::smem_addr(&wfull_bar[wb]), wph, abort_p);
+        good = good && ptx::mbar_wait(ptx::smem_addr(&full_bar[s]), ph, abort_p);
+        good = all_ok(good);
+        if (!good) {
+          fail(7000003);
+          break;
+        }
+        ptx::tc_fence_after();
+        if (ptx::elect_one()) {
+          const uint32_t base = stage(s);
+          const uint32_t sfa = sf_base + uint32_t(wb * C::kSfCols), sfb = sfa + 16;
+          const uint64_t da = ptx::smem_desc_k128(base), db = ptx::smem_desc_k128(base + C::kABytes);
+          const int left = a.K - kb * 2 * kBKBytes;  // elements of K from here on
+          const int w0 = kNv || first ? 0 : 2;
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks) {  // descriptors count in 16 bytes
+            const int w = w0 + (kNv ? ks : ks >> 1);
+            if (64 * ks < left)
+              ptx::mma_fp4<kNv>(d, da + 2 * ks, db + 2 * ks, ks & 1 ? idesc2 : idesc, sfa + 4 * w, sfb + C::kBCols * w,
+                                (kb | ks) != 0);
+          }
+          ptx::mma_commit(ptx::smem_addr(&empty_bar[s]));
+          if (last) ptx::mma_commit(ptx::smem_addr(&wempty_bar[wb]));
+          if (kb + 1 == KB) ptx::mma_commit(ptx::smem_addr(&accf_bar[buf]));
+        }
+        __syncwarp();
+        if (last && ++wb == C::kSfBufs) {
+          wb = 0;
+          wph ^= 1u;
+        }
+        if (++s == kStages) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+      if (!good) break;
+    }
+    if (ptx::elect_one()) ptx::mma_commit(ptx::smem_addr(&drain_bar));
+    __syncwarp();
+    ptx::mbar_wait(ptx::smem_addr(&drain_bar), 0, nullptr);
+  } else if (warp == 2) {
+    // ------------------------------------------------ scales to shared memory
+    int s = 0, issued = 0;
+    uint32_t ph = 0;
+    for (long long t = blockIdx.x; t < ntiles && all_ok(!*abort_p); t += gridDim.x) {
+      const Tile ti = tile_at(t);
+      const int boxes = (ti.rows + kBoxRows - 1) / kBoxRows;
+      const uint32_t bytes = uint32_t((kBM + boxes * kBoxRows) * kSlotRow);
+      for (int x = 0; x < stride; x += kSlotRow) {
+        if (!all_ok(ptx::mbar_wait(ptx::smem_addr(&sempty_bar[s]), ph ^ 1u, abort_p))) {
+          fail(7000004);
+          break;
+        }
+        if (ptx::elect_one()) {
+          const uint32_t bar = ptx::smem_addr(&sfull_bar[s]);
+          const uint32_t dst = ptx::smem_addr(smem) + C::kScaleAt + s * C::kSlotBytes;
+          ptx::mbar_arrive_expect_tx(bar, bytes);
+          ptx::tma_load_3d(dst, &maps.wscales, x, ti.m0, ti.e, bar);
+          for (int b = 0; b < boxes; ++b)
+            ptx::tma_load_2d(dst + (kBM + b * kBoxRows) * kSlotRow, &maps.tscales, x, ti.row0 + b * kBoxRows, bar);
+        }
+        __syncwarp();
+        issued = min(issued + 1, kSlots);
+        if (++s == kSlots) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+    }
+    for (int i = 0; i < issued; ++i) {
+      if (--s < 0) {
+        s = kSlots - 1;
+        ph ^= 1u;
+      }
+      ptx::mbar_wait(ptx::smem_addr(&sfull_bar[s]), ph, nullptr);
+    }
+  } else if (warp >= 4 && warp < 8) {
+    // ------------------------------------------------ scales to TMEM
+    const int blocks = a.K / (kNv ? 16 : 32);
+    const uint32_t quarter = tmem + (uint32_t(32 * (warp & 3)) << 16) + 2 * kTN;
+    int s = 0, wb = 0;
+    uint32_t ph = 0, wph = 0;
+    for (long long t = blockIdx.x; t < ntiles && all_ok(!*abort_p); t += gridDim.x) {
+      const Tile ti = tile_at(t);
+      const int nb = (ti.rows + 31) / 32;
+      for (int ci = 0; ci < chunks; ++ci) {
+        bool good = true;
+        if (ci % 2 == 0) good = ptx::mbar_wait(ptx::smem_addr(&sfull_bar[s]), ph, abort_p);
+        good = good && ptx::mbar_wait(ptx::smem_addr(&wempty_bar[wb]), wph ^ 1u, abort_p);
+        if (!all_ok(good)) {
+          fail(7000006);
+          break;
+        }
+        ptx::tc_fence_after();
+        const uint8_t* raw = smem + C::kScaleAt + s * C::kSlotBytes;
+        const int left = blocks - 16 * ci;
+        // 16 scale bytes of row 32 c + lane (32-byte swizzle: the halves of
+        // rows 4-7 of every 8 change places), without what lies behind K
+        auto row_words = [&](int c) {
+          const int r = 32 * c + lane;
+          uint4 v = *reinterpret_cast<const uint4*>(raw + r * kSlotRow + (((ci & 1) ^ ((r >> 2) & 1)) << 4));
+          if (left < 16) {
+            uint32_t* p = &v.x;
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+              p[w] &= left >= 4 * w + 4 ? 0xffffffffu : left <= 4 * w ? 0u : (1u << (8 * (left - 4 * w))) - 1;
+          }
+          return v;
+        };
+        const uint32_t wa = quarter + uint32_t(wb * C::kSfCols), wt = wa + 16;
+        {
+          const uint4 v0 = row_words(0), v1 = row_words(1), v2 = row_words(2), v3 = row_words(3);
+          ptx::tmem_st4(wa, v0.x, v1.x, v2.x, v3.x);
+          ptx::tmem_st4(wa + 4, v0.y, v1.y, v2.y, v3.y);
+          ptx::tmem_st4(wa + 8, v0.z, v1.z, v2.z, v3.z);
+          ptx::tmem_st4(wa + 12, v0.w, v1.w, v2.w, v3.w);
+        }
+        for (int c = 0; c < nb; c += 2) {
+          const uint4 v0 = row_words(4 + c);
+          if (c + 1 < nb) {
+            const uint4 v1 = row_words(5 + c);
+            ptx::tmem_st2(wt + c, v0.x, v1.x);
+            ptx::tmem_st2(wt + C::kBCols + c, v0.y, v1.y);
+            ptx::tmem_st2(wt + 2 * C::kBCols + c, v0.z, v1.z);
+            ptx::tmem_st2(wt + 3 * C::kBCols + c, v0.w, v1.w);
+          } else {
+            ptx::tmem_st1(wt + c, v0.x);
+            ptx::tmem_st1(wt + C::kBCols + c, v0.y);
+            ptx::tmem_st1(wt + 2 * C::kBCols + c, v0.z);
+            ptx::tmem_st1(wt + 3 * C::kBCols + c, v0.w);
+          }
+        }
+        ptx::tmem_st_wait();
+        ptx::tc_fence_before();
+        __syncwarp();
+        const bool slot_done = (ci & 1) || ci + 1 == chunks;
+        if (lane == 0) {
+          ptx::mbar_arrive(ptx::smem_addr(&wfull_bar[wb]));
+          if (slot_done) ptx::mbar_arrive(ptx::smem_addr(&sempty_bar[s]));
+        }
+        if (slot_done && ++s == kSlots) {
+          s = 0;
+          ph ^= 1u;
+        }
+        if (++wb == C::kSfBufs) {
+          wb = 0;
+          wph ^= 1u;
+        }
+      }
+    }
+  } else if (warp >= 8) {
     // ------------------------------------------------ epilogue
-    const int q = warp & 3;  // TMEM lane quarter this warp may read
-    uint8_t* scratch = smem + kStages * C::kStageBytes + q * kScratch;
+    const int q = warp & 3;         // TMEM lane quarter this warp may read
+    const int half = (warp >> 2) & 1;  // every other 16 tokens
+    uint8_t* scratch = smem + C::kScratchAt + (warp - 8) * kScratch;
     OT* out = static_cast<OT*>(a.out);
     const float ga = a.a_tscale ? *a.a_tscale : 1.f;
     constexpr int kPieces = 2 * sizeof(OT);  // 16-byte pieces of a token's 32 values
@@ -366,7 +439,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant_
       }
       ptx::tc_fence_after();
       const uint32_t taddr = tmem + (uint32_t(32 * q) << 16) + uint32_t(buf * kTN);
-      for (int c0 = 0; c0 < ti.rows; c0 += 16) {
+      for (int c0 = 16 * half; c0 < ti.rows; c0 += 32) {
         uint32_t v[16];
         ptx::tmem_ld16(taddr + uint32_t(c0), v);
         ptx::tmem_ld_wait();
@@ -421,17 +494,17 @@ EncodeFn encoder() {
   return f;
 }
 
-// Codes [planes, rows, row_bytes] in boxes of 128 bytes x box_rows.
-bool code_map(CUtensorMap* map, const uint8_t* base, uint64_t row_bytes, uint64_t rows, uint64_t planes, int dims,
-              uint32_t box_rows) {
+// Bytes [planes, rows, row_bytes] in boxes of box_bytes x box_rows.
+bool byte_map(CUtensorMap* map, const uint8_t* base, uint64_t row_bytes, uint64_t rows, uint64_t planes, int dims,
+              uint32_t box_bytes, uint32_t box_rows) {
   const EncodeFn f = encoder();
   if (!f) return false;
   const cuuint64_t size[3] = {row_bytes, rows, planes};
   const cuuint64_t stride[2] = {row_bytes, row_bytes * rows};
-  const cuuint32_t box[3] = {kBKBytes, box_rows, 1}, step[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {box_bytes, box_rows, 1}, step[3] = {1, 1, 1};
   return f(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, cuuint32_t(dims), const_cast<uint8_t*>(base), size, stride, box, step,
-           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+           CU_TENSOR_MAP_INTERLEAVE_NONE, box_bytes == 32 ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_128B,
+           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 int sm_count() {
@@ -443,32 +516,32 @@ int sm_count() {
 }
 
 template <bool kNv, int kTN, int kStages, typename OT>
-cudaError_t run(const CUtensorMap& wm, const CUtensorMap& tm, const Args& a, cudaStream_t st) {
-  using C = Cfg<kNv, kTN, kStages>;
+cudaError_t run(const Maps& m, const Args& a, cudaStream_t st) {
+  using C = Cfg<kTN, kStages>;
   auto* kernel = fp4_gemm_kernel<kNv, kTN, kStages, OT>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   // at most this many tiles: every group with rows may end in a partial one
   const long long most = ((long long)a.R / kTN + (a.R < a.E ? a.R : a.E) + 1) * ((a.N + kBM - 1) / kBM);
   const int sms = sm_count();
-  kernel<<<unsigned(most < sms ? most : sms), kThreads, C::kSmem, st>>>(wm, tm, a);
+  kernel<<<unsigned(most < sms ? most : sms), kThreads, C::kSmem, st>>>(m, a);
   count_launches(1);
   return cudaGetLastError();
 }
 
 template <bool kNv, typename OT>
-cudaError_t run_tiles(const CUtensorMap& wm, const CUtensorMap& tm, const Args& a, cudaStream_t st) {
+cudaError_t run_tiles(const Maps& m, const Args& a, cudaStream_t st) {
   // few rows per expert: narrow tiles leave room for a ring twice as deep, and
   // the weights stream through it
-  if (a.R <= 32LL * a.E) return run<kNv, 32, 8, OT>(wm, tm, a, st);
-  return run<kNv, 192, 4, OT>(wm, tm, a, st);
+  if (a.R <= 32LL * a.E) return run<kNv, 32, 8, OT>(m, a, st);
+  return run<kNv, 192, 4, OT>(m, a, st);
 }
 
 template <bool kNv>
-cudaError_t run_out(int32_t dtype, const CUtensorMap& wm, const CUtensorMap& tm, const Args& a, cudaStream_t st) {
-  if (dtype == MOE_DT_BF16) return run_tiles<kNv, __nv_bfloat16>(wm, tm, a, st);
-  if (dtype == MOE_DT_FP16) return run_tiles<kNv, __half>(wm, tm, a, st);
-  return run_tiles<kNv, float>(wm, tm, a, st);
+cudaError_t run_out(int32_t dtype, const Maps& m, const Args& a, cudaStream_t st) {
+  if (dtype == MOE_DT_BF16) return run_tiles<kNv, __nv_bfloat16>(m, a, st);
+  if (dtype == MOE_DT_FP16) return run_tiles<kNv, __half>(m, a, st);
+  return run_tiles<kNv, float>(m, a, st);
 }
 
 }  // namespace
@@ -499,13 +572,17 @@ extern "C" moe_status moe_mxfp_matmul(const uint8_t* a_codes, const uint8_t* a_s
     return MOE_ERR_INVALID_ARG;
   const moe_status s = status_ws_check(ws, ws_bytes);
   if (s != MOE_OK) return s;
-  CUtensorMap wm, tm;
-  if (!code_map(&wm, b_codes, K / 2, N, E, 3, kBM) || !code_map(&tm, a_codes, K / 2, R, 1, 2, kBoxRows))
+  Maps m;
+  const int S = scale_stride(format == MOE_FP_NV, K);
+  if (!byte_map(&m.wcodes, b_codes, K / 2, N, E, 3, kBKBytes, kBM) ||
+      !byte_map(&m.tcodes, a_codes, K / 2, R, 1, 2, kBKBytes, kBoxRows) ||
+      !byte_map(&m.wscales, b_scales, S, N, E, 3, kSlotRow, kBM) ||
+      !byte_map(&m.tscales, a_scales, S, R, 1, 2, kSlotRow, kBoxRows))
     return MOE_ERR_CUDA;
-  Args a{a_scales, b_scales, a_tensor_scale, b_tensor_scale, offsets, out, ws_at<WsHeader>(ws, 0), R, K, N, E,
+  Args a{a_tensor_scale, b_tensor_scale, offsets, out, ws_at<WsHeader>(ws, 0), R, K, N, E,
          int((size_t(N) * size) % 16 == 0 && ptr_aligned(out, 16))};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = format == MOE_FP_NV ? run_out<true>(out_dtype, wm, tm, a, st)
-                                            : run_out<false>(out_dtype, wm, tm, a, st);
+  const cudaError_t e = format == MOE_FP_NV ? run_out<true>(out_dtype, m, a, st)
+                                            : run_out<false>(out_dtype, m, a, st);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
