@@ -295,148 +295,152 @@ MOE_STATUS_BYTES = 8704
 FORMATS = {"mx": 1, "nv": 2}  # MOE_FP_MX, MOE_FP_NV
 _FP_BLOCK = {"mx": 32, "nv": 16}
 MOE_FP_SWIGLU = 1
-_DTYPES = {"bfloat16": 1, "float16": 2, "float32": 3, "uint8": 4}
-_dtype_codes = {}  # torch.dtype -> MOE_DT_*, filled on first use
+_torch = None  # the torch module and what the calls below need of it, on first use
+_codes = {}    # torch.dtype -> MOE_DT_*
+_raw_stream = None
+
+
+def _rt():
+    """Set up on the first call: importing torch here keeps the module's import
+    light, and a call's checks cost less than its launch."""
+    global _torch, _raw_stream
+    import torch
+    _torch = torch
+    _codes.update({torch.bfloat16: 1, torch.float16: 2, torch.float32: 3, torch.uint8: 4})
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return torch
 
 
 def new_status_workspace(device="cuda"):
     """The smallest workspace: the status word of the calls below, cleared."""
-    import torch
-    return torch.zeros(MOE_STATUS_BYTES, dtype=torch.uint8, device=device)
+    return (_torch or _rt()).zeros(MOE_STATUS_BYTES, dtype=_torch.uint8, device=device)
 
 
-def _dtype(t, name, bytes_ok=False):
+def _device():
+    """The device whose stream a call runs on, and on which its tensors must
+    be: the current one (-1, the CPU, in tests without a device)."""
+    t = _torch or _rt()
+    return t.cuda.current_device() if REQUIRE_CUDA else -1
+
+
+def _on(stream, dev):
+    """Address of the stream a call runs on: the current one, or `stream`."""
+    if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(dev)
+        return _torch.cuda.current_stream().cuda_stream
+    d = getattr(stream, "device", None)
+    if REQUIRE_CUDA and d is not None and d.index is not None and d.index != dev:
+        raise ValueError(f"stream: on device {d.index}, the tensors are on {dev}")
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _p(t, name, dev, dtype, shape):
+    """Address of a tensor argument: on the current device, contiguous, of the
+    given torch dtype and exactly the given shape."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    if t is None:
+        raise ValueError(f"{name}: required (the call takes no NULL here)")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: must be a CUDA tensor on the current device {dev}, got {t.device}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: dtype {t.dtype} where the call takes {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    raise ValueError(f"{name}: must be contiguous")
+
+
+def _opt(t, name, dev, dtype, shape):
+    return None if t is None else _p(t, name, dev, dtype, shape)
+
+
+def _count(t, name, dev):
+    """A device int32 scalar (or one-element slice), or None."""
+    return None if t is None else _p(t.reshape(-1), name, dev, _torch.int32, (1,))
+
+
+def _rows_of(t, name, bytes_ok=False):
+    """(rows, columns, torch dtype, MOE_DT_* code) of the matrix a call goes by."""
+    if t is None:
+        raise ValueError(f"{name}: required (the call takes no NULL here)")
+    n, m = _shape2(t, name)
     d = t.dtype
-    c = _dtype_codes.get(d)
-    if c is None:
-        c = _dtype_codes[d] = _DTYPES.get(str(d).replace("torch.", ""), 0)
+    c = _codes.get(d, 0)
     if c == 0 or (c == 4 and not bytes_ok):
         raise TypeError(f"{name}: dtype {d} where the call takes bf16, fp16 or fp32{' or uint8' if bytes_ok else ''}")
-    return c
+    return n, m, d, c
 
 
-class _Call:
-    """The tensor arguments of one call: all on the current CUDA device (its
-    stream is the one the kernels run on), contiguous, of the expected type and
-    exactly the expected shape."""
-
-    __slots__ = ("device",)
-
-    def __init__(self):
-        if REQUIRE_CUDA:
-            import torch
-            self.device = torch.cuda.current_device()
-
-    def ptr(self, t, name, shape=None, dtype=None):
-        """Address of `t`; `dtype` is a MOE_DT_* code, or the name of a torch
-        dtype the header fixes."""
-        if t is None:
-            raise ValueError(f"{name}: required (the call takes no NULL here)")
-        if REQUIRE_CUDA and t.get_device() != self.device:
-            raise ValueError(f"{name}: must be a CUDA tensor on the current device {self.device}, got {t.device}")
-        if isinstance(dtype, int):
-            if _dtype(t, name, True) != dtype:
-                raise TypeError(f"{name}: dtype {t.dtype} differs from the call's other rows")
-        elif dtype is not None and _type_names(t) != dtype:
-            raise TypeError(f"{name}: dtype {t.dtype} where the call takes {dtype}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name}: must be contiguous")
-        if shape is not None and t.shape != shape:
-            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-        return t.data_ptr()
-
-    def opt(self, t, name, shape, dtype):
-        return None if t is None else self.ptr(t, name, shape, dtype)
-
-    def count(self, t, name):
-        """A device int32 scalar (or one-element slice), or None."""
-        return None if t is None else self.ptr(t.reshape(-1), name, (1,), "int32")
-
-    def ws(self, t):
-        return self.ptr(t, "ws", None, "uint8"), t.numel()
-
-    def stream(self, stream):
-        if stream is None:
-            import torch
-            return torch.cuda.current_stream().cuda_stream
-        d = getattr(stream, "device", None)
-        if REQUIRE_CUDA and d is not None and d.index is not None and d.index != self.device:
-            raise ValueError(f"stream: on device {d.index}, the tensors are on {self.device}")
-        return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-
-
-_names = {}  # torch.dtype -> its name without "torch."
-
-
-def _type_names(t):
-    d = t.dtype
-    n = _names.get(d)
-    if n is None:
-        n = _names[d] = str(d).replace("torch.", "")
-    return n
-
-
-def _pairs(inv_perm, T):
-    """k of an inv_perm [T*k] (or [T, k])."""
+def _pairs(inv_perm, T, dev):
+    """(address, k) of an inv_perm [T*k] (or [T, k])."""
     n = inv_perm.numel()
-    if T == 0 or n % T or n == 0:
+    if n % T or n == 0:
         raise ValueError(f"inv_perm: {n} pairs for {T} tokens")
-    return n // T
+    return _p(inv_perm, "inv_perm", dev, _torch.int32, inv_perm.shape), n // T
+
+
+def _status_ws(ws, dev):
+    return _p(ws, "ws", dev, _torch.uint8, None if ws is None else ws.shape)
 
 
 def permute(x, inv_perm, x_perm, ws, stream=None):
     """moe_permute: x [T, H] to the rows x_perm [T*k, H] sorted by expert."""
-    c = _Call()
-    T, H = _shape2(x, "x")
+    dev = _device()
+    T, H, d, code = _rows_of(x, "x", True)
     if T == 0:
         return
-    k, dt = _pairs(inv_perm, T), _dtype(x, "x", True)
-    w, n = c.ws(ws)
-    _check("moe_permute", LIB.moe_permute(c.ptr(x, "x"), dt, T, H, k, c.ptr(inv_perm, "inv_perm", None, "int32"),
-                                          c.ptr(x_perm, "x_perm", (T * k, H), dt), w, n, c.stream(stream)))
+    inv, k = _pairs(inv_perm, T, dev)
+    st = LIB.moe_permute(_p(x, "x", dev, d, (T, H)), code, T, H, k, inv, _p(x_perm, "x_perm", dev, d, (T * k, H)),
+                         _status_ws(ws, dev), ws.numel(), _on(stream, dev))
+    if st:
+        raise MoeError("moe_permute", st)
 
 
 def permute_grad(dx_perm, inv_perm, dx, ws, stream=None):
     """moe_permute_grad: dx [T, H], the sum of each token's rows of dx_perm."""
-    c = _Call()
-    T, H = _shape2(dx, "dx")
+    dev = _device()
+    T, H, d, code = _rows_of(dx, "dx")
     if T == 0:
         return
-    k, dt = _pairs(inv_perm, T), _dtype(dx, "dx")
-    w, n = c.ws(ws)
-    _check("moe_permute_grad", LIB.moe_permute_grad(c.ptr(dx_perm, "dx_perm", (T * k, H), dt), dt, T, H, k,
-                                                    c.ptr(inv_perm, "inv_perm", None, "int32"), c.ptr(dx, "dx"), w, n,
-                                                    c.stream(stream)))
+    inv, k = _pairs(inv_perm, T, dev)
+    st = LIB.moe_permute_grad(_p(dx_perm, "dx_perm", dev, d, (T * k, H)), code, T, H, k, inv,
+                              _p(dx, "dx", dev, d, (T, H)), _status_ws(ws, dev), ws.numel(), _on(stream, dev))
+    if st:
+        raise MoeError("moe_permute_grad", st)
 
 
 def unpermute(y_perm, inv_perm, topk_w, out, ws, stream=None):
     """moe_unpermute: out [T, H], each token's rows weighted by topk_w [T, k]."""
-    c = _Call()
-    T, H = _shape2(out, "out")
+    dev = _device()
+    T, H, d, code = _rows_of(out, "out")
     if T == 0:
         return
-    k, dt = _pairs(inv_perm, T), _dtype(out, "out")
-    w, n = c.ws(ws)
-    _check("moe_unpermute", LIB.moe_unpermute(c.ptr(y_perm, "y_perm", (T * k, H), dt), dt, T, H, k,
-                                              c.ptr(inv_perm, "inv_perm", None, "int32"),
-                                              c.ptr(topk_w, "topk_w", (T, k), "float32"), c.ptr(out, "out"), w, n,
-                                              c.stream(stream)))
+    inv, k = _pairs(inv_perm, T, dev)
+    st = LIB.moe_unpermute(_p(y_perm, "y_perm", dev, d, (T * k, H)), code, T, H, k, inv,
+                           _p(topk_w, "topk_w", dev, _torch.float32, (T, k)), _p(out, "out", dev, d, (T, H)),
+                           _status_ws(ws, dev), ws.numel(), _on(stream, dev))
+    if st:
+        raise MoeError("moe_unpermute", st)
 
 
 def unpermute_grad(dout, y_perm, inv_perm, topk_w, dy_perm, dtopk_w, ws, stream=None):
     """moe_unpermute_grad: the gradients of y_perm and topk_w from dout [T, H]."""
-    c = _Call()
-    T, H = _shape2(dout, "dout")
+    dev = _device()
+    T, H, d, code = _rows_of(dout, "dout")
     if T == 0:
         return
-    k, dt = _pairs(inv_perm, T), _dtype(dout, "dout")
-    w, n = c.ws(ws)
-    _check("moe_unpermute_grad",
-           LIB.moe_unpermute_grad(c.ptr(dout, "dout"), c.ptr(y_perm, "y_perm", (T * k, H), dt), dt, T, H, k,
-                                  c.ptr(inv_perm, "inv_perm", None, "int32"),
-                                  c.ptr(topk_w, "topk_w", (T, k), "float32"),
-                                  c.ptr(dy_perm, "dy_perm", (T * k, H), dt),
-                                  c.ptr(dtopk_w, "dtopk_w", (T, k), "float32"), w, n, c.stream(stream)))
+    inv, k = _pairs(inv_perm, T, dev)
+    f = _torch.float32
+    st = LIB.moe_unpermute_grad(_p(dout, "dout", dev, d, (T, H)), _p(y_perm, "y_perm", dev, d, (T * k, H)), code, T, H,
+                                k, inv, _p(topk_w, "topk_w", dev, f, (T, k)),
+                                _p(dy_perm, "dy_perm", dev, d, (T * k, H)), _p(dtopk_w, "dtopk_w", dev, f, (T, k)),
+                                _status_ws(ws, dev), ws.numel(), _on(stream, dev))
+    if st:
+        raise MoeError("moe_unpermute_grad", st)
 
 
 def _format(fmt):
@@ -461,48 +465,51 @@ def _stride(cols, fmt):  # moe_mxfp_scale_stride without a call
 def mxfp_quantize(x, codes, scales, fmt, tensor_scale=None, swiglu=False, rows_dev=None, stream=None):
     """moe_mxfp_quantize: x [rows, cols] (with swiglu: gate | up [rows, 2*cols])
     to codes [rows, cols/2] and scales [rows, mxfp_scale_stride(cols, fmt)]."""
-    c, f = _Call(), _format(fmt)
-    rows, cols = _shape2(x, "x")
+    dev, f = _device(), _format(fmt)
+    rows, wide, d, code = _rows_of(x, "x")
+    cols = wide
     if swiglu:
-        if cols % 2:
-            raise ValueError(f"x: {cols} columns are no gate and up halves")
-        cols //= 2
-    _check("moe_mxfp_quantize",
-           LIB.moe_mxfp_quantize(c.ptr(x, "x"), _dtype(x, "x"), rows, cols, f, MOE_FP_SWIGLU if swiglu else 0,
-                                 c.opt(tensor_scale, "tensor_scale", (1,), "float32"), c.count(rows_dev, "rows_dev"),
-                                 c.ptr(codes, "codes", (rows, cols // 2), "uint8"),
-                                 c.ptr(scales, "scales", (rows, _stride(cols, fmt)), "uint8"), c.stream(stream)))
+        if wide % 2:
+            raise ValueError(f"x: {wide} columns are no gate and up halves")
+        cols = wide // 2
+    u8 = _torch.uint8
+    st = LIB.moe_mxfp_quantize(_p(x, "x", dev, d, (rows, wide)), code, rows, cols, f, MOE_FP_SWIGLU if swiglu else 0,
+                               _opt(tensor_scale, "tensor_scale", dev, _torch.float32, (1,)),
+                               _count(rows_dev, "rows_dev", dev), _p(codes, "codes", dev, u8, (rows, cols // 2)),
+                               _p(scales, "scales", dev, u8, (rows, _stride(cols, fmt))), _on(stream, dev))
+    if st:
+        raise MoeError("moe_mxfp_quantize", st)
 
 
 def mxfp_dequantize(codes, scales, out, fmt, tensor_scale=None, rows_dev=None, stream=None):
     """moe_mxfp_dequantize: the values of codes and scales into out [rows, cols]."""
-    c, f = _Call(), _format(fmt)
-    rows, cols = _shape2(out, "out")
-    _check("moe_mxfp_dequantize",
-           LIB.moe_mxfp_dequantize(c.ptr(codes, "codes", (rows, cols // 2), "uint8"),
-                                   c.ptr(scales, "scales", (rows, _stride(cols, fmt)), "uint8"), rows, cols, f,
-                                   c.opt(tensor_scale, "tensor_scale", (1,), "float32"),
-                                   c.count(rows_dev, "rows_dev"), c.ptr(out, "out"), _dtype(out, "out"),
-                                   c.stream(stream)))
+    dev, f = _device(), _format(fmt)
+    rows, cols, d, code = _rows_of(out, "out")
+    u8 = _torch.uint8
+    st = LIB.moe_mxfp_dequantize(_p(codes, "codes", dev, u8, (rows, cols // 2)),
+                                 _p(scales, "scales", dev, u8, (rows, _stride(cols, fmt))), rows, cols, f,
+                                 _opt(tensor_scale, "tensor_scale", dev, _torch.float32, (1,)),
+                                 _count(rows_dev, "rows_dev", dev), _p(out, "out", dev, d, (rows, cols)), code,
+                                 _on(stream, dev))
+    if st:
+        raise MoeError("moe_mxfp_dequantize", st)
 
 
 def mxfp_matmul(a_codes, a_scales, b_codes, b_scales, out, fmt, ws, offsets=None, a_tensor_scale=None,
                 b_tensor_scale=None, stream=None):
     """moe_mxfp_matmul: rows a [R, K] times their expert's b [E, N, K] into out
     [R, N]; offsets [E+1] as moe_dispatch writes them (None: E = 1)."""
-    c, f = _Call(), _format(fmt)
-    R, N = _shape2(out, "out")
-    if b_codes.dim() != 3:
-        raise ValueError(f"b_codes: shape {tuple(b_codes.shape)}, expected [E, N, K/2]")
+    dev, f = _device(), _format(fmt)
+    R, N, d, code = _rows_of(out, "out")
+    if b_codes is None or b_codes.dim() != 3:
+        raise ValueError("b_codes: expected [E, N, K/2]")
     E, _, half = b_codes.shape
-    S = _stride(2 * half, fmt)
-    w, n = c.ws(ws)
-    _check("moe_mxfp_matmul",
-           LIB.moe_mxfp_matmul(c.ptr(a_codes, "a_codes", (R, half), "uint8"),
-                               c.ptr(a_scales, "a_scales", (R, S), "uint8"),
-                               c.opt(a_tensor_scale, "a_tensor_scale", (1,), "float32"), R, 2 * half,
-                               c.ptr(b_codes, "b_codes", (E, N, half), "uint8"),
-                               c.ptr(b_scales, "b_scales", (E, N, S), "uint8"),
-                               c.opt(b_tensor_scale, "b_tensor_scale", (E,), "float32"), E, N,
-                               c.opt(offsets, "offsets", (E + 1,), "int32"), f, c.ptr(out, "out"),
-                               _dtype(out, "out"), w, n, c.stream(stream)))
+    S, u8, f32 = _stride(2 * half, fmt), _torch.uint8, _torch.float32
+    st = LIB.moe_mxfp_matmul(_p(a_codes, "a_codes", dev, u8, (R, half)), _p(a_scales, "a_scales", dev, u8, (R, S)),
+                             _opt(a_tensor_scale, "a_tensor_scale", dev, f32, (1,)), R, 2 * half,
+                             _p(b_codes, "b_codes", dev, u8, (E, N, half)), _p(b_scales, "b_scales", dev, u8, (E, N, S)),
+                             _opt(b_tensor_scale, "b_tensor_scale", dev, f32, (E,)), E, N,
+                             _opt(offsets, "offsets", dev, _torch.int32, (E + 1,)), f, _p(out, "out", dev, d, (R, N)),
+                             code, _status_ws(ws, dev), ws.numel(), _on(stream, dev))
+    if st:
+        raise MoeError("moe_mxfp_matmul", st)

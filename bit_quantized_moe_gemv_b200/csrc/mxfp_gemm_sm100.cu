@@ -7,24 +7,27 @@
 // the MMA (kind::mxf4 for MX, kind::mxf4nvf4 for NV); products are exact and
 // sums stay in fp32 in TMEM until the one rounding of the epilogue.
 //
-// One persistent CTA per SM, 16 warps:
+// One persistent CTA per SM, 20 warps:
 //   warp 0       codes: TMA tiles of 128 bytes (256 elements of K) per row,
 //                128-byte swizzle, kStages deep
 //   warp 1       MMA issuer, four K = 64 MMAs per stage
 //   warp 2       scales: TMA tiles of 32 bytes per row, kSlots deep
-//   warps 4-7    scale words from shared memory into TMEM, where the MMA reads
+//   warps 4-11   scale words from shared memory into TMEM, where the MMA reads
 //                them: lane (row % 32), column (row / 32), the same in all four
-//                lane quarters, so that each warp fills its own. They are
+//                lane quarters, so that each warp fills its own; two groups
+//                of four take turns. They are
 //                written from registers because the rows' words are 4 bytes
 //                of a row-major matrix, which no copy into TMEM can gather; on
 //                the way the bytes behind K become 0
-//   warps 8-15   epilogue: TMEM -> registers -> smem (transposed) -> global,
+//   warps 12-19  epilogue: TMEM -> registers -> smem (transposed) -> global,
 //                on the other of two accumulators
 //
 // Tiles: every CTA sums up the experts' token tiles (offsets are on the
-// device) in shared memory and takes tiles b, b + grid, ... of the list
-// "expert, token tile, 128 weight rows": neighbours share the tokens, and an
-// expert's weights are read from HBM once, later token tiles hit L2.
+// device) and takes tiles b, b + grid, ... of the list "expert, token tile, 128
+// weight rows": neighbours share the tokens, and an expert's weights are read
+// from HBM once, later token tiles hit L2. What a tile is (expert, rows) is
+// worked out by all threads at once for the next kListed tiles of the CTA: the
+// search and the divisions cost a single warp about 900 cycles a tile.
 #include <cuda.h>
 
 #include <atomic>
@@ -40,11 +43,16 @@ namespace {
 constexpr int kBM = 128;       // weight rows per tile
 constexpr int kBKBytes = 128;  // code bytes of a row per stage: 256 elements
 constexpr int kBoxRows = 32;   // token rows per TMA box
-constexpr int kThreads = 512;
-constexpr int kEpiWarps = 8, kScaleWarps = 4;
+constexpr int kThreads = 640;
+constexpr int kEpiWarps = 8, kScaleWarps = 8;
 constexpr int kSlotRow = 32;   // scale bytes of a row per slot
 constexpr int kSlots = 3;
-constexpr int kScratch = 2048;  // epilogue staging per warp: 16 tokens x 32 rows x 4 bytes
+#ifndef PF
+#define PF 8
+#endif
+constexpr int kPrefetch = PF;
+constexpr int kListed = 256;  // tiles listed at a time
+constexpr int kScratch = 2048;  // epilogue staging per warp: 32 weight rows of 32 (16 bits) or 16 tokens
 
 // kTN: tokens per tile (a multiple of 32); kStages: ring depth.
 template <int kTN, int kStages>
@@ -55,7 +63,7 @@ struct Cfg {
   static constexpr int kSlotBytes = (kBM + kTN) * kSlotRow;
   // TMEM: two accumulators of kTN columns, then buffers of the scale words of
   // 16 bytes of each row: 4 x 4 columns of weights, 4 x kBCols of tokens
-  static constexpr int kBCols = (kBBlocks + 3) / 4 * 4;
+  static constexpr int kBCols = kBBlocks > 4 ? 8 : 4;
   static constexpr int kSfCols = 4 * (4 + kBCols);
   static constexpr int kSfBufs = (512 - 2 * kTN) / kSfCols >= 4 ? 4 : 2;
   static constexpr int kCols = 2 * kTN + kSfBufs * kSfCols;
@@ -81,7 +89,7 @@ struct Maps {
   CUtensorMap wcodes, tcodes, wscales, tscales;
 };
 
-struct Tile {
+struct alignas(16) Tile {
   int e, m0, row0, rows;
 };
 
@@ -103,15 +111,20 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
   __shared__ int off_sh[kMaxE + 1];    // first row of each expert
   __shared__ int first_sh[kMaxE + 1];  // first token tile of each expert
   __shared__ int wsum_sh[kThreads / 32];
+  __shared__ Tile list_sh[kListed];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort_p = &abort_sh;
 
-  if (threadIdx.x == 0) {
-    ptx::tma_prefetch_map(&maps.wcodes);
-    ptx::tma_prefetch_map(&maps.tcodes);
-    ptx::tma_prefetch_map(&maps.wscales);
-    ptx::tma_prefetch_map(&maps.tscales);
+  // ---- the running sum of token tiles; barriers and TMEM meanwhile
+  constexpr int kPer = (kMaxE + kThreads - 1) / kThreads;
+  int row_at[kPer + 1];
+#pragma unroll
+  for (int i = 0; i <= kPer; ++i) {
+    const int e = threadIdx.x * kPer + i;
+    row_at[i] = e > a.E ? 0 : a.offsets ? a.offsets[e] : e ? a.R : 0;
+  }
+  if (warp == 0 && lane == 0) {
     for (int s = 0; s < kStages; ++s) {
       ptx::mbar_init(ptx::smem_addr(&full_bar[s]), 1);
       ptx::mbar_init(ptx::smem_addr(&empty_bar[s]), 1);
@@ -121,7 +134,7 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
       ptx::mbar_init(ptx::smem_addr(&sempty_bar[s]), kScaleWarps);
     }
     for (int b = 0; b < C::kSfBufs; ++b) {
-      ptx::mbar_init(ptx::smem_addr(&wfull_bar[b]), kScaleWarps);
+      ptx::mbar_init(ptx::smem_addr(&wfull_bar[b]), kScaleWarps / 2);
       ptx::mbar_init(ptx::smem_addr(&wempty_bar[b]), 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -131,47 +144,47 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
     ptx::mbar_init(ptx::smem_addr(&drain_bar), 1);
     abort_sh = 0;
     ptx::mbar_init_fence();
-  }
-  if (warp == 1) {
+  } else if (warp == 1) {
     ptx::tmem_alloc(ptx::smem_addr(&tmem_base_sh), C::kTmemCols);
     ptx::tmem_relinquish();
+  } else if (warp == 2 && lane == 0) {
+    ptx::tma_prefetch_map(&maps.wcodes);
+    ptx::tma_prefetch_map(&maps.tcodes);
+    ptx::tma_prefetch_map(&maps.wscales);
+    ptx::tma_prefetch_map(&maps.tscales);
   }
-  // ---- the tile list: offsets, then the running sum of token tiles
-  for (int e = threadIdx.x; e <= a.E; e += kThreads) off_sh[e] = a.offsets ? a.offsets[e] : (e ? a.R : 0);
-  __syncthreads();
   bool ok = true;
-  {
-    constexpr int kPer = (kMaxE + kThreads - 1) / kThreads;
-    int cnt[kPer], sum = 0;
+  int cnt[kPer], sum = 0;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int e = threadIdx.x * kPer + i;
-      cnt[i] = 0;
-      if (e < a.E) {
-        const int lo = off_sh[e], hi = off_sh[e + 1];
-        if (lo < 0 || hi < lo || hi > a.R)
-          ok = false;
-        else
-          cnt[i] = token_tiles(hi - lo, kTN);
-      }
-      sum += cnt[i];
+  for (int i = 0; i < kPer; ++i) {
+    const int e = threadIdx.x * kPer + i;
+    cnt[i] = 0;
+    if (e < a.E) {
+      if (row_at[i] < 0 || row_at[i + 1] < row_at[i] || row_at[i + 1] > a.R)
+        ok = false;
+      else
+        cnt[i] = token_tiles(row_at[i + 1] - row_at[i], kTN);
     }
-    int incl = sum;
+    sum += cnt[i];
+  }
+  int incl = sum;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    if (lane == 31) wsum_sh[warp] = incl;
-    ok = !__syncthreads_or(!ok);
-    int base = incl - sum;
-    for (int w = 0; w < warp; ++w) base += wsum_sh[w];
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) wsum_sh[warp] = incl;
+  ok = !__syncthreads_or(!ok);
+  int base = incl - sum;
+  for (int w = 0; w < warp; ++w) base += wsum_sh[w];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int e = threadIdx.x * kPer + i;
-      if (e <= a.E) first_sh[e] = base;
-      base += cnt[i];
+  for (int i = 0; i < kPer; ++i) {
+    const int e = threadIdx.x * kPer + i;
+    if (e <= a.E) {
+      off_sh[e] = row_at[i];
+      first_sh[e] = base;
     }
+    base += cnt[i];
   }
   if (!ok && threadIdx.x == 0) flag_error(a.hdr, MOE_ERR_DEVICE_FAULT, -1);
   ptx::tc_fence_before();
@@ -181,291 +194,330 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
   const int MT = (a.N + kBM - 1) / kBM;
   const int KB = (a.K + 2 * kBKBytes - 1) / (2 * kBKBytes);
   const int stride = scale_stride(kNv, a.K);
-  const int chunks = stride / 16;             // 16 scale bytes per row: one TMEM buffer
-  constexpr int kChunkStages = kNv ? 1 : 2;   // code stages they cover
-  const long long ntiles = ok ? (long long)first_sh[a.E] * MT : 0;
+  const int chunks = stride / 16;  // 16 scale bytes per row: one TMEM buffer
+  const int ntiles = ok ? first_sh[a.E] * MT : 0;
+  const int mine = int(blockIdx.x) < ntiles ? (ntiles - 1 - int(blockIdx.x)) / int(gridDim.x) + 1 : 0;
 
-  // Called by whole warps: the last expert whose first tile is <= tt, by two
-  // rounds of 32 comparisons.
-  auto tile_at = [&](long long t) {
-    Tile r;
-    const int tt = int(t / MT);
-    r.m0 = int(t - (long long)tt * MT) * kBM;
-    const int c = __popc(__ballot_sync(0xffffffffu, 32 * lane < a.E && first_sh[32 * lane] <= tt)) - 1;
-    const int e = 32 * c + lane;
-    r.e = 32 * c + __popc(__ballot_sync(0xffffffffu, e < a.E && first_sh[e] <= tt)) - 1;
-    const int lo = off_sh[r.e], rows = off_sh[r.e + 1] - lo;
-    const int nt = first_sh[r.e + 1] - first_sh[r.e], i = tt - first_sh[r.e];
-    // tiles of one size, a multiple of 16 (at most kTN, so none is empty)
-    const int per = nt == 1 ? rows : ((rows + nt - 1) / nt + 15) & ~15;
-    r.row0 = lo + i * per;
-    r.rows = min(per, rows - i * per);
-    return r;
+  auto tile_at = [&](int t) {
+    const int tt = int(uint32_t(t) / uint32_t(MT));
+    int e = 0, hi = a.E;  // the last expert whose first token tile is <= tt
+    while (hi - e > 1) {
+      const int mid = (e + hi) >> 1;
+      if (first_sh[mid] <= tt)
+        e = mid;
+      else
+        hi = mid;
+    }
+    const int lo = off_sh[e], rows = off_sh[e + 1] - lo, nt = first_sh[e + 1] - first_sh[e], i = tt - first_sh[e];
+    // token tiles of one size, a multiple of 16 (at most kTN, so none is empty)
+    const int per = nt == 1 ? rows : (int(uint32_t(rows + nt - 1) / uint32_t(nt)) + 15) & ~15;
+    return Tile{e, (t - tt * MT) * kBM, lo + i * per, min(per, rows - i * per)};
   };
   auto fail = [&](int where) {
     flag_error(a.hdr, MOE_ERR_TIMEOUT, where);
     *abort_p = 1;
   };
-  // For roles that run as whole warps: the lanes agree, so that none leaves a
-  // loop alone when a wait gives up.
-  auto all_ok = [&](bool good) { return __all_sync(0xffffffffu, good) != 0; };
+  // One lane polls, the warp follows and agrees on the outcome, so that no
+  // lane leaves a loop alone when a wait gives up.
+  auto warp_wait = [&](uint64_t& bar, uint32_t parity) {
+    bool got = true;
+    if (lane == 0) got = ptx::mbar_wait(ptx::smem_addr(&bar), parity, abort_p);
+    return __all_sync(0xffffffffu, got) != 0;
+  };
+  auto warp_wait_sleep = [&](uint64_t& bar, uint32_t parity) {
+    bool got = true;
+    if (lane == 0) got = ptx::mbar_wait_sleep(ptx::smem_addr(&bar), parity, abort_p, 32);
+    return __all_sync(0xffffffffu, got) != 0;
+  };
   auto stage = [&](int s) { return ptx::smem_addr(smem) + uint32_t(s) * C::kStageBytes; };
 
-  if (warp == 0) {
-    // ------------------------------------------------ codes
-    int s = 0, issued = 0;
-    uint32_t ph = 0;
-    for (long long t = blockIdx.x; t < ntiles && all_ok(!*abort_p); t += gridDim.x) {
-      const Tile ti = tile_at(t);
-      const int boxes = (ti.rows + kBoxRows - 1) / kBoxRows;
-      const uint32_t bytes = uint32_t(C::kABytes + boxes * kBoxRows * kBKBytes);
-      for (int kb = 0; kb < KB; ++kb) {
-        if (!all_ok(ptx::mbar_wait(ptx::smem_addr(&empty_bar[s]), ph ^ 1u, abort_p))) {
-          fail(7000001);
-          break;
-        }
-        if (ptx::elect_one()) {
+  // State that a role carries from one list of tiles to the next: its place in
+  // its ring and that place's phase, the same of the TMEM scale buffers, tiles
+  // done, copies it may have in flight.
+  int s = 0, wb = 0, it = 0, issued = 0;
+  uint32_t ph = 0, wph = 0;
+
+  for (int first_tile = 0; first_tile < mine; first_tile += kListed) {
+    const int n = min(kListed, mine - first_tile);
+    if (int(threadIdx.x) < n)
+      list_sh[threadIdx.x] = tile_at(int(blockIdx.x) + (first_tile + int(threadIdx.x)) * int(gridDim.x));
+    __syncthreads();
+    if (warp == 0 && ptx::elect_one()) {
+      // ------------------------------------------------ codes
+      int pi = 0, pkb = 0;  // the weights are brought to L2 up to this tile and stage
+      int ahead = 0;
+      for (int i = 0; i < n; ++i) {
+        const Tile ti = list_sh[i];
+        const int boxes = (ti.rows + kBoxRows - 1) / kBoxRows;
+        const uint32_t bytes = uint32_t(C::kABytes + boxes * kBoxRows * kBKBytes);
+        int kb = 0;
+        for (; kb < KB; ++kb) {
+          for (; ahead < kStages + kPrefetch && pi < n; ++ahead) {
+            if (i > 0 || ahead >= kStages) ptx::tma_prefetch_3d(&maps.wcodes, pkb * kBKBytes, list_sh[pi].m0, list_sh[pi].e);
+            if (++pkb == KB) {
+              pkb = 0;
+              ++pi;
+            }
+          }
+          --ahead;
+          if (!ptx::mbar_wait(ptx::smem_addr(&empty_bar[s]), ph ^ 1u, abort_p)) break;
           const uint32_t bar = ptx::smem_addr(&full_bar[s]), dst = stage(s);
           ptx::mbar_arrive_expect_tx(bar, bytes);
           ptx::tma_load_3d(dst, &maps.wcodes, kb * kBKBytes, ti.m0, ti.e, bar);
           for (int b = 0; b < boxes; ++b)
             ptx::tma_load_2d(dst + C::kABytes + b * kBoxRows * kBKBytes, &maps.tcodes, kb * kBKBytes,
                              ti.row0 + b * kBoxRows, bar);
+          issued = min(issued + 1, kStages);
+          if (++s == kStages) {
+            s = 0;
+            ph ^= 1u;
+          }
         }
-        __syncwarp();
-        issued = min(issued + 1, kStages);
-        if (++s == kStages) {
-          s = 0;
-          ph ^= 1u;
-        }
-      }
-    }
-    // no copy may be in flight when the CTA leaves
-    for (int i = 0; i < issued; ++i) {
-      if (--s < 0) {
-        s = kStages - 1;
-        ph ^= 1u;
-      }
-      ptx::mbar_wait(ptx::smem_addr(&full_bar[s]), ph, nullptr);
-    }
-  } else if (warp == 1) {
-    // ------------------------------------------------ MMA issuer
-    int s = 0, it = 0;
-    uint32_t ph = 0;
-    int wb = 0;  // scale buffer
-    uint32_t wph = 0;
-    const uint32_t sf_base = tmem + 2 * kTN;
-    for (long long t = blockIdx.x; t < ntiles && all_ok(!*abort_p); t += gridDim.x, ++it) {
-      const Tile ti = tile_at(t);
-      const int N = (ti.rows + 15) & ~15;
-      const int buf = it & 1;
-      if (!all_ok(ptx::mbar_wait(ptx::smem_addr(&acce_bar[buf]), (uint32_t(it >> 1) & 1u) ^ 1u, abort_p))) {
-        fail(7000002);
-        break;
-      }
-      const uint32_t d = tmem + uint32_t(buf * kTN);
-      const uint32_t idesc = ptx::idesc_fp4<kNv>(kBM, N, 0), idesc2 = ptx::idesc_fp4<kNv>(kBM, N, kNv ? 0 : 2);
-      bool good = true;
-      for (int kb = 0; kb < KB; ++kb) {
-        const bool first = kb % kChunkStages == 0, last = kb % kChunkStages == kChunkStages - 1 || kb + 1 == KB;
-        if (first) good = ptx::mbar_wait(ptx::smem_addr(&wfull_bar[wb]), wph, abort_p);
-        good = good && ptx::mbar_wait(ptx::smem_addr(&full_bar[s]), ph, abort_p);
-        good = all_ok(good);
-        if (!good) {
-          fail(7000003);
+        if (kb < KB) {
+          fail(7000001);
           break;
         }
-        ptx::tc_fence_after();
-        if (ptx::elect_one()) {
-          const uint32_t base = stage(s);
-          const uint32_t sfa = sf_base + uint32_t(wb * C::kSfCols), sfb = sfa + 16;
-          const uint64_t da = ptx::smem_desc_k128(base), db = ptx::smem_desc_k128(base + C::kABytes);
-          const int left = a.K - kb * 2 * kBKBytes;  // elements of K from here on
-          const int w0 = kNv || first ? 0 : 2;
+      }
+    } else if (warp == 1 && ptx::elect_one()) {
+      // ------------------------------------------------ MMA issuer
+      const uint32_t sf_base = tmem + 2 * kTN;
+      const uint64_t da0 = ptx::smem_desc_k128(stage(0));
+      for (int i = 0; i < n; ++i, ++it) {
+        const int N = (list_sh[i].rows + 15) & ~15;
+        const uint32_t d = tmem + uint32_t((it & 1) * kTN);
+        const uint32_t idesc = ptx::idesc_fp4<kNv>(kBM, N, 0), idesc2 = ptx::idesc_fp4<kNv>(kBM, N, kNv ? 0 : 2);
+        const uint32_t bcols = N > 128 ? 8 : 4;
+        bool good = ptx::mbar_wait(ptx::smem_addr(&acce_bar[it & 1]), (uint32_t(it >> 1) & 1u) ^ 1u, abort_p);
+        for (int kb = 0; kb < KB && good; ++kb) {
+          const bool second = !kNv && (kb & 1);  // MX: two stages share the scale words of a buffer
+          if (!second) good = ptx::mbar_wait(ptx::smem_addr(&wfull_bar[wb]), wph, abort_p);
+          if (!(good && ptx::mbar_wait(ptx::smem_addr(&full_bar[s]), ph, abort_p))) {
+            good = false;
+            break;
+          }
+          ptx::tc_fence_after();
+          // descriptors count in 16 bytes
+          const uint64_t da = da0 + uint32_t(s * (C::kStageBytes / 16)), db = da + C::kABytes / 16;
+          const uint32_t sfa = sf_base + uint32_t(wb * C::kSfCols) + (second ? 8 : 0);
+          const uint32_t sfb = sf_base + uint32_t(wb * C::kSfCols) + 16 + (second ? 2 * bcols : 0);
+          const int steps = (a.K - kb * 2 * kBKBytes + 63) / 64;  // K steps that are left
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks) {  // descriptors count in 16 bytes
-            const int w = w0 + (kNv ? ks : ks >> 1);
-            if (64 * ks < left)
-              ptx::mma_fp4<kNv>(d, da + 2 * ks, db + 2 * ks, ks & 1 ? idesc2 : idesc, sfa + 4 * w, sfb + C::kBCols * w,
-                                (kb | ks) != 0);
+          for (int ks = 0; ks < 4; ++ks) {
+            constexpr int kPerWord = kNv ? 1 : 2;
+            if (ks < steps)
+              ptx::mma_fp4<kNv>(d, da + 2 * ks, db + 2 * ks, ks & 1 ? idesc2 : idesc, sfa + 4 * (ks / kPerWord),
+                                sfb + bcols * (ks / kPerWord), (kb | ks) != 0);
           }
           ptx::mma_commit(ptx::smem_addr(&empty_bar[s]));
-          if (last) ptx::mma_commit(ptx::smem_addr(&wempty_bar[wb]));
-          if (kb + 1 == KB) ptx::mma_commit(ptx::smem_addr(&accf_bar[buf]));
+          if (kNv || second || kb + 1 == KB) {
+            ptx::mma_commit(ptx::smem_addr(&wempty_bar[wb]));
+            if (++wb == C::kSfBufs) {
+              wb = 0;
+              wph ^= 1u;
+            }
+          }
+          if (++s == kStages) {
+            s = 0;
+            ph ^= 1u;
+          }
         }
-        __syncwarp();
-        if (last && ++wb == C::kSfBufs) {
-          wb = 0;
-          wph ^= 1u;
-        }
-        if (++s == kStages) {
-          s = 0;
-          ph ^= 1u;
-        }
-      }
-      if (!good) break;
-    }
-    if (ptx::elect_one()) ptx::mma_commit(ptx::smem_addr(&drain_bar));
-    __syncwarp();
-    ptx::mbar_wait(ptx::smem_addr(&drain_bar), 0, nullptr);
-  } else if (warp == 2) {
-    // ------------------------------------------------ scales to shared memory
-    int s = 0, issued = 0;
-    uint32_t ph = 0;
-    for (long long t = blockIdx.x; t < ntiles && all_ok(!*abort_p); t += gridDim.x) {
-      const Tile ti = tile_at(t);
-      const int boxes = (ti.rows + kBoxRows - 1) / kBoxRows;
-      const uint32_t bytes = uint32_t((kBM + boxes * kBoxRows) * kSlotRow);
-      for (int x = 0; x < stride; x += kSlotRow) {
-        if (!all_ok(ptx::mbar_wait(ptx::smem_addr(&sempty_bar[s]), ph ^ 1u, abort_p))) {
-          fail(7000004);
+        if (!good) {
+          fail(7000002);
           break;
         }
-        if (ptx::elect_one()) {
+        ptx::mma_commit(ptx::smem_addr(&accf_bar[it & 1]));
+      }
+    } else if (warp == 2 && ptx::elect_one()) {
+      // ------------------------------------------------ scales to shared memory
+      for (int i = 0; i < n; ++i) {
+        const Tile ti = list_sh[i];
+        const int boxes = (ti.rows + kBoxRows - 1) / kBoxRows;
+        const uint32_t bytes = uint32_t((kBM + boxes * kBoxRows) * kSlotRow);
+        int x = 0;
+        for (; x < stride; x += kSlotRow) {
+          if (!ptx::mbar_wait(ptx::smem_addr(&sempty_bar[s]), ph ^ 1u, abort_p)) break;
           const uint32_t bar = ptx::smem_addr(&sfull_bar[s]);
           const uint32_t dst = ptx::smem_addr(smem) + C::kScaleAt + s * C::kSlotBytes;
           ptx::mbar_arrive_expect_tx(bar, bytes);
           ptx::tma_load_3d(dst, &maps.wscales, x, ti.m0, ti.e, bar);
           for (int b = 0; b < boxes; ++b)
             ptx::tma_load_2d(dst + (kBM + b * kBoxRows) * kSlotRow, &maps.tscales, x, ti.row0 + b * kBoxRows, bar);
+          issued = min(issued + 1, kSlots);
+          if (++s == kSlots) {
+            s = 0;
+            ph ^= 1u;
+          }
         }
-        __syncwarp();
-        issued = min(issued + 1, kSlots);
-        if (++s == kSlots) {
-          s = 0;
-          ph ^= 1u;
+        if (x < stride) {
+          fail(7000003);
+          break;
         }
       }
-    }
-    for (int i = 0; i < issued; ++i) {
-      if (--s < 0) {
-        s = kSlots - 1;
-        ph ^= 1u;
+    } else if (warp >= 4 && warp < 12) {
+      // ------------------------------------------------ scales to TMEM
+      const int blocks = a.K / (kNv ? 16 : 32);
+      const uint32_t quarter = tmem + (uint32_t(32 * (warp & 3)) << 16) + 2 * kTN;
+      const int group = (warp >> 2) - 1;  // takes every other buffer
+      bool good = true;
+      for (int i = 0; i < n && good; ++i) {
+        const int rows = list_sh[i].rows;
+        const int nb = (rows + 31) / 32;
+        for (int ci = 0; ci < chunks; ++ci) {
+          const bool slot_done = (ci & 1) || ci + 1 == chunks;
+          if ((wb & 1) == group) {
+            good = warp_wait(sfull_bar[s], ph) && warp_wait(wempty_bar[wb], wph ^ 1u);
+            if (!good) {
+              fail(7000004);
+              break;
+            }
+            // 16 scale bytes of row 32 c + lane (32-byte swizzle: the halves
+            // of rows 4-7 of every 8 change places)
+            const uint8_t* raw = smem + C::kScaleAt + s * C::kSlotBytes + lane * kSlotRow +
+                                 (((ci & 1) ^ ((lane >> 2) & 1)) << 4);
+            uint4 v[4 + C::kBBlocks];
+#pragma unroll
+            for (int c = 0; c < 4 + C::kBBlocks; ++c)
+              if (c < 4 + nb) v[c] = *reinterpret_cast<const uint4*>(raw + 32 * c * kSlotRow);
+            const int left = blocks - 16 * ci;
+            if (left < 16) {  // what lies behind K counts as 0
+              uint32_t m[4];
+#pragma unroll
+              for (int w = 0; w < 4; ++w)
+                m[w] = left >= 4 * w + 4 ? 0xffffffffu : left <= 4 * w ? 0u : (1u << (8 * (left - 4 * w))) - 1;
+#pragma unroll
+              for (int c = 0; c < 4 + C::kBBlocks; ++c) {
+                v[c].x &= m[0];
+                v[c].y &= m[1];
+                v[c].z &= m[2];
+                v[c].w &= m[3];
+              }
+            }
+            ptx::tc_fence_after();
+            const uint32_t at = quarter + uint32_t(wb * C::kSfCols);
+            auto store16 = [&](uint32_t to, int c0) {  // 4 words of 4 blocks
+              uint32_t r[16];
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const uint4 q = c0 + c < 4 + C::kBBlocks ? v[c0 + c] : make_uint4(0, 0, 0, 0);
+                r[c] = q.x;
+                r[4 + c] = q.y;
+                r[8 + c] = q.z;
+                r[12 + c] = q.w;
+              }
+              ptx::tmem_st16(to, r);
+            };
+            store16(at, 0);
+            if (C::kBBlocks <= 4 || rows <= 128) {
+              store16(at + 16, 4);
+            } else {
+              uint32_t r[32];
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {
+                const uint4 q = c < C::kBBlocks ? v[4 + c] : make_uint4(0, 0, 0, 0);
+                r[c] = q.x;
+                r[8 + c] = q.y;
+                r[16 + c] = q.z;
+                r[24 + c] = q.w;
+              }
+              ptx::tmem_st32(at + 16, r);
+            }
+            ptx::tmem_st_wait();
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&wfull_bar[wb]));
+          }
+          if (slot_done) {  // both groups give every slot back
+            if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&sempty_bar[s]));
+            if (++s == kSlots) {
+              s = 0;
+              ph ^= 1u;
+            }
+          }
+          if (++wb == C::kSfBufs) {
+            wb = 0;
+            wph ^= 1u;
+          }
+        }
       }
-      ptx::mbar_wait(ptx::smem_addr(&sfull_bar[s]), ph, nullptr);
-    }
-  } else if (warp >= 4 && warp < 8) {
-    // ------------------------------------------------ scales to TMEM
-    const int blocks = a.K / (kNv ? 16 : 32);
-    const uint32_t quarter = tmem + (uint32_t(32 * (warp & 3)) << 16) + 2 * kTN;
-    int s = 0, wb = 0;
-    uint32_t ph = 0, wph = 0;
-    for (long long t = blockIdx.x; t < ntiles && all_ok(!*abort_p); t += gridDim.x) {
-      const Tile ti = tile_at(t);
-      const int nb = (ti.rows + 31) / 32;
-      for (int ci = 0; ci < chunks; ++ci) {
-        bool good = true;
-        if (ci % 2 == 0) good = ptx::mbar_wait(ptx::smem_addr(&sfull_bar[s]), ph, abort_p);
-        good = good && ptx::mbar_wait(ptx::smem_addr(&wempty_bar[wb]), wph ^ 1u, abort_p);
-        if (!all_ok(good)) {
-          fail(7000006);
+    } else if (warp >= 12) {
+      // ------------------------------------------------ epilogue
+      constexpr int kTok = sizeof(OT) == 2 && kTN > 32 ? 32 : 16;  // tokens staged at a time
+      constexpr int kPieces = 2 * sizeof(OT);                      // 16-byte pieces of a token's 32 values
+      constexpr int kPerPiece = 16 / sizeof(OT);
+      const int q = warp & 3;             // TMEM lane quarter this warp may read
+      const int half = (warp - 12) >> 2;  // two warps per quarter take turns
+      uint8_t* scratch = smem + C::kScratchAt + (warp - 12) * kScratch;
+      OT* out = static_cast<OT*>(a.out);
+      const float ga = a.a_tscale ? *a.a_tscale : 1.f;
+      for (int i = 0; i < n; ++i, ++it) {
+        const Tile ti = list_sh[i];
+        const float alpha = a.b_tscale ? ga * a.b_tscale[ti.e] : ga;
+        const int n0 = ti.m0 + 32 * q;
+        if (!warp_wait_sleep(accf_bar[it & 1], uint32_t(it >> 1) & 1u)) {
+          fail(7000005);
           break;
         }
         ptx::tc_fence_after();
-        const uint8_t* raw = smem + C::kScaleAt + s * C::kSlotBytes;
-        const int left = blocks - 16 * ci;
-        // 16 scale bytes of row 32 c + lane (32-byte swizzle: the halves of
-        // rows 4-7 of every 8 change places), without what lies behind K
-        auto row_words = [&](int c) {
-          const int r = 32 * c + lane;
-          uint4 v = *reinterpret_cast<const uint4*>(raw + r * kSlotRow + (((ci & 1) ^ ((r >> 2) & 1)) << 4));
-          if (left < 16) {
-            uint32_t* p = &v.x;
+        const uint32_t taddr = tmem + (uint32_t(32 * q) << 16) + uint32_t((it & 1) * kTN);
+        for (int c0 = kTok * half; c0 < ti.rows; c0 += 2 * kTok) {
+          uint32_t v[kTok];
+          if constexpr (kTok == 32)
+            ptx::tmem_ld32(taddr + uint32_t(c0), v);
+          else
+            ptx::tmem_ld16(taddr + uint32_t(c0), v);
+          ptx::tmem_ld_wait();
+          if (a.vec_store) {
+            OT* sc = reinterpret_cast<OT*>(scratch);
 #pragma unroll
-            for (int w = 0; w < 4; ++w)
-              p[w] &= left >= 4 * w + 4 ? 0xffffffffu : left <= 4 * w ? 0u : (1u << (8 * (left - 4 * w))) - 1;
-          }
-          return v;
-        };
-        const uint32_t wa = quarter + uint32_t(wb * C::kSfCols), wt = wa + 16;
-        {
-          const uint4 v0 = row_words(0), v1 = row_words(1), v2 = row_words(2), v3 = row_words(3);
-          ptx::tmem_st4(wa, v0.x, v1.x, v2.x, v3.x);
-          ptx::tmem_st4(wa + 4, v0.y, v1.y, v2.y, v3.y);
-          ptx::tmem_st4(wa + 8, v0.z, v1.z, v2.z, v3.z);
-          ptx::tmem_st4(wa + 12, v0.w, v1.w, v2.w, v3.w);
-        }
-        for (int c = 0; c < nb; c += 2) {
-          const uint4 v0 = row_words(4 + c);
-          if (c + 1 < nb) {
-            const uint4 v1 = row_words(5 + c);
-            ptx::tmem_st2(wt + c, v0.x, v1.x);
-            ptx::tmem_st2(wt + C::kBCols + c, v0.y, v1.y);
-            ptx::tmem_st2(wt + 2 * C::kBCols + c, v0.z, v1.z);
-            ptx::tmem_st2(wt + 3 * C::kBCols + c, v0.w, v1.w);
-          } else {
-            ptx::tmem_st1(wt + c, v0.x);
-            ptx::tmem_st1(wt + C::kBCols + c, v0.y);
-            ptx::tmem_st1(wt + 2 * C::kBCols + c, v0.z);
-            ptx::tmem_st1(wt + 3 * C::kBCols + c, v0.w);
+            for (int j = 0; j < kTok; ++j) sc[j * 32 + lane] = from_f32<OT>(__uint_as_float(v[j]) * alpha);
+            __syncwarp();
+            OT* o = out + (size_t)(ti.row0 + c0 + lane / kPieces) * a.N + n0 + lane % kPieces * kPerPiece;
+            const bool in = n0 + lane % kPieces * kPerPiece < a.N;
+#pragma unroll
+            for (int p = 0; p < kTok * kPieces / 32; ++p) {
+              const int tok = lane / kPieces + p * (32 / kPieces);
+              if (in && c0 + tok < ti.rows)
+                *reinterpret_cast<uint4*>(o + (size_t)p * (32 / kPieces) * a.N) =
+                    *reinterpret_cast<const uint4*>(scratch + (p * 32 + lane) * 16);
+            }
+            __syncwarp();
+          } else if (n0 + lane < a.N) {
+            OT* o = out + (size_t)(ti.row0 + c0) * a.N + n0 + lane;
+#pragma unroll
+            for (int j = 0; j < kTok; ++j)
+              if (c0 + j < ti.rows) o[(size_t)j * a.N] = from_f32<OT>(__uint_as_float(v[j]) * alpha);
           }
         }
-        ptx::tmem_st_wait();
         ptx::tc_fence_before();
         __syncwarp();
-        const bool slot_done = (ci & 1) || ci + 1 == chunks;
-        if (lane == 0) {
-          ptx::mbar_arrive(ptx::smem_addr(&wfull_bar[wb]));
-          if (slot_done) ptx::mbar_arrive(ptx::smem_addr(&sempty_bar[s]));
-        }
-        if (slot_done && ++s == kSlots) {
-          s = 0;
-          ph ^= 1u;
-        }
-        if (++wb == C::kSfBufs) {
-          wb = 0;
-          wph ^= 1u;
-        }
+        if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&acce_bar[it & 1]));
       }
     }
-  } else if (warp >= 8) {
-    // ------------------------------------------------ epilogue
-    const int q = warp & 3;         // TMEM lane quarter this warp may read
-    const int half = (warp >> 2) & 1;  // every other 16 tokens
-    uint8_t* scratch = smem + C::kScratchAt + (warp - 8) * kScratch;
-    OT* out = static_cast<OT*>(a.out);
-    const float ga = a.a_tscale ? *a.a_tscale : 1.f;
-    constexpr int kPieces = 2 * sizeof(OT);  // 16-byte pieces of a token's 32 values
-    constexpr int kPerPiece = 16 / sizeof(OT);
-    int it = 0;
-    for (long long t = blockIdx.x; t < ntiles && all_ok(!*abort_p); t += gridDim.x, ++it) {
-      const Tile ti = tile_at(t);
-      const float alpha = a.b_tscale ? ga * a.b_tscale[ti.e] : ga;
-      const int buf = it & 1;
-      const int n0 = ti.m0 + 32 * q;
-      if (!all_ok(ptx::mbar_wait_sleep(ptx::smem_addr(&accf_bar[buf]), uint32_t(it >> 1) & 1u, abort_p, 32))) {
-        fail(7000005);
-        break;
+    if (warp < 3) {  // the elected lane's state, whichever lane is elected next
+      const int from = ptx::elected_lane();
+      s = __shfl_sync(0xffffffffu, s, from);
+      ph = __shfl_sync(0xffffffffu, ph, from);
+      wb = __shfl_sync(0xffffffffu, wb, from);
+      wph = __shfl_sync(0xffffffffu, wph, from);
+      it = __shfl_sync(0xffffffffu, it, from);
+      issued = __shfl_sync(0xffffffffu, issued, from);
+    }
+    __syncthreads();  // the list may be written again
+    if (*abort_p) break;
+  }
+
+  // no copy and no MMA may be in flight when the CTA leaves
+  if (warp == 1 && ptx::elect_one()) {
+    ptx::mma_commit(ptx::smem_addr(&drain_bar));
+    ptx::mbar_wait(ptx::smem_addr(&drain_bar), 0, nullptr);
+  } else if (warp == 0 || warp == 2) {
+    const int depth = warp == 0 ? kStages : kSlots;
+    for (int i = 0; i < issued; ++i) {
+      if (--s < 0) {
+        s = depth - 1;
+        ph ^= 1u;
       }
-      ptx::tc_fence_after();
-      const uint32_t taddr = tmem + (uint32_t(32 * q) << 16) + uint32_t(buf * kTN);
-      for (int c0 = 16 * half; c0 < ti.rows; c0 += 32) {
-        uint32_t v[16];
-        ptx::tmem_ld16(taddr + uint32_t(c0), v);
-        ptx::tmem_ld_wait();
-        if (a.vec_store) {
-          OT* sc = reinterpret_cast<OT*>(scratch);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) sc[i * 32 + lane] = from_f32<OT>(__uint_as_float(v[i]) * alpha);
-          __syncwarp();
-#pragma unroll
-          for (int p = lane; p < 16 * kPieces; p += 32) {
-            const int tok = p / kPieces, n = n0 + p % kPieces * kPerPiece;
-            if (c0 + tok < ti.rows && n < a.N)
-              *reinterpret_cast<uint4*>(out + (size_t)(ti.row0 + c0 + tok) * a.N + n) =
-                  *reinterpret_cast<const uint4*>(scratch + p * 16);
-          }
-          __syncwarp();
-        } else if (n0 + lane < a.N) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (c0 + i < ti.rows)
-              out[(size_t)(ti.row0 + c0 + i) * a.N + n0 + lane] = from_f32<OT>(__uint_as_float(v[i]) * alpha);
-        }
-      }
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&acce_bar[buf]));
+      ptx::mbar_wait(ptx::smem_addr(warp == 0 ? &full_bar[s] : &sfull_bar[s]), ph, nullptr);
     }
   }
   __syncthreads();
@@ -559,8 +611,9 @@ extern "C" moe_status moe_mxfp_matmul(const uint8_t* a_codes, const uint8_t* a_s
   const int size = dtype_size(out_dtype);
   if (size < 2) return MOE_ERR_UNSUPPORTED;
   // one expert's codes stay below the 2^40 bytes a tensor map can stride over
+  // and the tiles are counted in 32 bits
   if (R < 0 || R > (1 << 30) || E < 1 || E > kMaxE || N < 1 || N > kMaxFpCols || K < 32 || K % 32 || K > kMaxFpCols ||
-      (int64_t)N * K >= (1LL << 41))
+      (int64_t)N * K >= (1LL << 41) || (int64_t)R * N > (1LL << 40))
     return MOE_ERR_INVALID_ARG;
   if (!offsets && E != 1) return MOE_ERR_INVALID_ARG;
   if (format == MOE_FP_MX && (a_tensor_scale || b_tensor_scale)) return MOE_ERR_INVALID_ARG;
