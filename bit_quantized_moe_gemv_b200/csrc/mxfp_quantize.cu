@@ -9,11 +9,11 @@
 //
 // Rounding is decided on the exact quotient, so that codes do not depend on
 // how a division was rounded: MX scales by powers of two, which is exact; in
-// the other cases the fp32 quotient is used unless it lies within kNear units
-// in the last place of a rounding border, where the exact comparison of x
-// with border * scale decides (an fma for plain NV, whose border * s fits 7
-// bits; 64-bit arithmetic for the SwiGLU input, whose fp32 value carries a few
-// units of error).
+// the other cases the fp32 quotient is rounded twice, lowered and raised by its
+// largest error, and where the codes differ the exact comparison of x with
+// border * scale decides (an fma for plain NV, whose border * s fits
+// 7 bits; 64-bit arithmetic for the SwiGLU input). Approximate reciprocals and
+// exponentials are therefore enough in the common path.
 //
 // HBM bound: 8 elements per thread by 16-byte loads, a block's 4 (MX) or 2
 // (NV) lanes exchange their maxima by shuffles, codes leave as one 32-bit word
@@ -29,10 +29,14 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-// Largest error of a computed quotient, in units in the last place: expf 2,
-// the sum 0.5 and the division 0.5 of silu, the product 0.5, the scale's
-// product and reciprocal 1, the last product 0.5; taken three times.
-constexpr uint32_t kNear = 16;
+// How far, in units of 2^-23 of its value, a computed quotient may be from the
+// exact one. Plain NV: scale product and reciprocal (1 each), products (0.5).
+// SwiGLU adds the approximate exp (the rounding of gate * log2(e), whose value
+// is below 128, gives 0.35 * 128; ex2 itself 2), the sum, the reciprocal and
+// two products (2.5). The bounds are rounded up by half.
+constexpr float kOffPlain = 4.f * 0x1p-23f, kOffSwiglu = 80.f * 0x1p-23f;
+// Beyond this sum of exponentials a reciprocal may have left the normal range.
+constexpr float kExpSum = 0x1p120f;
 
 // Rows in chunks of 8 elements: chunk g is chunk (g % per_row) of row
 // (g / per_row). For fewer than 2^31 chunks the quotient comes from one
@@ -67,49 +71,108 @@ __device__ __forceinline__ long long rows_in_use(const int* rows_dev, long long 
   return n < 0 ? 0 : n < rows ? n : rows;
 }
 
+// 8 elements in one or two 16-byte words.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
-  constexpr int kVecs = sizeof(T) / 2;  // 16-byte loads
-  Vec<T, 8 / kVecs> q[kVecs];
+struct Eight {
+  static constexpr int kN = 16 / sizeof(T), kVecs = 8 / kN;
+  Pack<T, kN> p[kVecs];
+  __device__ __forceinline__ void load(const T* x) {
 #pragma unroll
-  for (int i = 0; i < kVecs; ++i) q[i] = reinterpret_cast<const Vec<T, 8 / kVecs>*>(p)[i];
+    for (int i = 0; i < kVecs; ++i) p[i] = reinterpret_cast<const Pack<T, kN>*>(x)[i];
+  }
+  __device__ __forceinline__ void store(T* x) const {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = to_f32(q[i / (8 / kVecs)].v[i % (8 / kVecs)]);
-}
+    for (int i = 0; i < kVecs; ++i) reinterpret_cast<Pack<T, kN>*>(x)[i] = p[i];
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      float q[kN];
+      p[i].get(q);
+#pragma unroll
+      for (int j = 0; j < kN; ++j) v[i * kN + j] = q[j];
+    }
+  }
+  __device__ __forceinline__ void set(const float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      float q[kN];
+#pragma unroll
+      for (int j = 0; j < kN; ++j) q[j] = v[i * kN + j];
+      p[i].set(q);
+    }
+  }
+};
 
-__device__ __forceinline__ double swiglu_f64(float gate, float up) {
+// Kept out of line: rarely called, and its registers would halve the warps in
+// flight of the common path.
+__device__ __noinline__ double swiglu_f64(float gate, float up) {
   return double(gate) / (1.0 + exp(-double(gate))) * double(up);
 }
-
-// The value with `keep` mantissa bits nearest to v, and whether v lies in the
-// range [lo, hi) that has borders and so near to it that an error of kNear
-// units may have moved v across.
-__device__ __forceinline__ bool near_border(float v, int keep, float lo_v, float hi_v, float* border) {
-  const uint32_t u = __float_as_uint(v), low = (1u << (23 - keep)) - 1;
-  const uint32_t b = (u + (low >> 1) + 1) & ~low;
-  *border = __uint_as_float(b);
-  return u + kNear - b <= 2 * kNear && v >= lo_v && v < hi_v;
+__device__ __forceinline__ float ex2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
-// v moved to the side of the border that `diff` (x minus border * scale) says.
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+// The value with `keep` mantissa bits nearest to v.
+__device__ __forceinline__ float border_of(float v, int keep) {
+  const uint32_t low = (1u << (23 - keep)) - 1;
+  return __uint_as_float((__float_as_uint(v) + (low >> 1) + 1) & ~low);
+}
+// The float next to the border on the side that `diff` (x minus border *
+// scale) says, or the border itself.
 __device__ __forceinline__ float beside(float border, double diff) {
   return __uint_as_float(__float_as_uint(border) + (diff > 0) - (diff < 0));
 }
+__device__ __forceinline__ uint32_t e2m1x2(float low, float high) {
+  return __nv_cvt_float2_to_fp4x2(make_float2(low, high), __NV_E2M1, cudaRoundNearest);
+}
+__device__ __forceinline__ uint32_t e2m1_word(const float (&h)[8], float f) {
+  return e2m1x2(h[0] * f, h[1] * f) | e2m1x2(h[2] * f, h[3] * f) << 8 | e2m1x2(h[4] * f, h[5] * f) << 16 |
+         e2m1x2(h[6] * f, h[7] * f) << 24;
+}
 
 // Codes and the scale byte of one block whose lanes hold 8 elements each.
-template <typename T, bool kNv, bool kSwiglu>
-__device__ __forceinline__ void quantise8(const float (&x)[8], const float (&up)[8], float g, uint32_t* codes,
-                                          uint32_t* scale) {
+// g: the tensor scale, inv6g about 1 / (6 g).
+template <bool kNv, bool kSwiglu>
+__device__ __forceinline__ void quantise8(const float (&x)[8], const float (&up)[8], float g, float inv6g,
+                                          uint32_t* codes, uint32_t* scale) {
   constexpr int kLanes = kNv ? 2 : 4;
+  constexpr float kOff = kSwiglu ? kOffSwiglu : kOffPlain;
   float h[8];
-  uint32_t top = 0;  // bits of |h| order like the values, NaN above infinity
+  float top = 0.f, exps = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    h[i] = kSwiglu ? silu_f32(x[i]) * up[i] : x[i];
-    top = max(top, __float_as_uint(h[i]) & 0x7fffffffu);
+    if (kSwiglu) {
+      const float e = ex2_approx(x[i] * -1.4426950408889634f);
+      h[i] = x[i] * rcp_approx(1.f + e) * up[i];
+      exps += e;
+    } else {
+      h[i] = x[i];
+    }
+  }
+  if (kSwiglu) {
+    if (!(exps < kExpSum)) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[i] = float(swiglu_f64(x[i], up[i]));
+    }
   }
 #pragma unroll
-  for (int o = 1; o < kLanes; o *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-  const bool bad = top >= 0x7f800000u;
+  for (int i = 0; i < 8; ++i) top = max_nan(top, fabsf(h[i]));
+#pragma unroll
+  for (int o = 1; o < kLanes; o *= 2) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const bool bad = !(top <= 3.402823466e38f);  // infinite or NaN
 
   // largest |h| in 64 bits, for the rare border cases of the scale
   auto top_f64 = [&]() {
@@ -121,133 +184,159 @@ __device__ __forceinline__ void quantise8(const float (&x)[8], const float (&up)
     return t;
   };
 
-  float s, inv;  // block scale without g, and 1 / (s g)
+  float s, inv;  // block scale without g, and about 1 / (s g)
   if (kNv) {
-    float q = __uint_as_float(top) / (6.f * g), border;
-    const bool near = !bad && near_border(q, 4, 0x1p-11f, 512.f, &border);
+    float q = top * inv6g;
+    __nv_fp8_storage_t b = __nv_cvt_float_to_fp8(q * (1.f - kOff), __NV_SATFINITE, __NV_E4M3);
+    const bool near = !bad && b != __nv_cvt_float_to_fp8(q * (1.f + kOff), __NV_SATFINITE, __NV_E4M3);
     if (__any_sync(0xffffffffu, near)) {
       const double t = top_f64();
-      if (near) q = beside(border, t - double(border) * 6.0 * double(g));
-    }
-    const __nv_fp8_storage_t b = __nv_cvt_float_to_fp8(q, __NV_SATFINITE, __NV_E4M3);
-    *scale = bad ? 0x7fu : b;
-    s = f16_to_f32(__nv_cvt_fp8_to_halfraw(b, __NV_E4M3).x);
-    inv = s > 0.f ? 1.f / (s * g) : 0.f;
-  } else {
-    if (kSwiglu) {
-      const uint32_t up_ = (top + kNear) & 0x7fffffu;  // small when top is about a power of two
-      const bool near = !bad && up_ <= 2 * kNear && top > 0x01000000u;  // below, the scale byte is 0 either way
-      if (__any_sync(0xffffffffu, near)) {
-        const double t = top_f64();
-        if (near) {
-          const uint32_t b = (top + kNear) & 0xff800000u;  // the power of two
-          top = t < double(__uint_as_float(b)) ? b - 1 : b;
-        }
+      if (near) {
+        const float border = border_of(q, 4);  // borders between E4M3 values have 4 mantissa bits
+        q = beside(border, t - double(border) * 6.0 * double(g));
+        b = __nv_cvt_float_to_fp8(q, __NV_SATFINITE, __NV_E4M3);
       }
     }
-    const int e = int(top >> 23) - 2;  // biased floor(log2), less E2M1's largest exponent
+    *scale = bad ? 0x7fu : b;
+    s = f16_to_f32(__nv_cvt_fp8_to_halfraw(b, __NV_E4M3).x);
+    inv = s > 0.f ? rcp_approx(s * g) : 0.f;
+  } else {
+    if (kSwiglu) {
+      // the exponent changes at a power of two (below 2^-124 the scale byte is 0 either way)
+      const uint32_t above = __float_as_uint(top * (1.f + kOff)) & 0xff800000u;
+      const bool near = !bad && __float_as_uint(top * (1.f - kOff)) < above && top > 0x1p-124f;
+      if (__any_sync(0xffffffffu, near)) {
+        const double t = top_f64();
+        if (near) top = t < double(__uint_as_float(above)) ? __uint_as_float(above - 1) : __uint_as_float(above);
+      }
+    }
+    const int e = int(__float_as_uint(top) >> 23) - 2;  // biased floor(log2), less E2M1's largest exponent
     *scale = bad ? 0xffu : uint32_t(max(e, 0));
-    s = 1.f;  // borders are compared in units of the scale below
+    s = 1.f;
     inv = __uint_as_float(uint32_t(254 - max(e, 0)) << 23);
   }
 
-  uint32_t word = 0;
+  uint32_t word = e2m1_word(h, kNv || kSwiglu ? inv * (1.f - kOff) : inv);
+  if (kNv || kSwiglu) {
+    // a code that the uncertainty of its quotient could change is decided exactly
+    const uint32_t differ = word ^ e2m1_word(h, inv * (1.f + kOff));
+    if (differ) {
+      const double unit = kNv ? double(s) * double(g) : 1.0 / double(inv);
 #pragma unroll
-  for (int i = 0; i < 8; i += 2) {
-    float v[2];
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      v[c] = fabsf(h[i + c]) * inv;
-      if (kNv || kSwiglu) {
-        float border;
-        if (near_border(v[c], 2, 0.125f, 8.f, &border)) {
-          if (kSwiglu) {
-            const double unit = kNv ? double(s) * double(g) : 1.0 / double(inv);
-            v[c] = beside(border, fabs(swiglu_f64(x[i + c], up[i + c])) - double(border) * unit);
-          } else {
-            v[c] = beside(border, fmaf(-(border * s), g, fabsf(h[i + c])));
-          }
+      for (int i = 0; i < 8; ++i) {
+        if (differ >> (4 * i) & 15u) {
+          const float border = border_of(fabsf(h[i]) * inv, 2);  // these borders have 2 mantissa bits
+          const float v = kSwiglu ? beside(border, fabs(swiglu_f64(x[i], up[i])) - double(border) * unit)
+                                  : beside(border, fmaf(-(border * s), g, fabsf(h[i])));
+          word = (word & ~(15u << (4 * i))) | (e2m1x2(copysignf(v, h[i]), 0.f) & 15u) << (4 * i);
         }
       }
-      v[c] = copysignf(v[c], h[i + c]);
     }
-    word |= uint32_t(__nv_cvt_float2_to_fp4x2(make_float2(v[0], v[1]), __NV_E2M1, cudaRoundNearest)) << (4 * i);
   }
   *codes = bad || (kNv && s == 0.f) ? 0u : word;
 }
 
 template <typename T, bool kNv, bool kSwiglu, int kUnroll>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
 quantize_kernel(const T* __restrict__ x, long long rows, Split sp, int scale_stride, const float* __restrict__ tscale,
                 const int* __restrict__ rows_dev, uint32_t* __restrict__ codes, uint8_t* __restrict__ scales) {
   constexpr int kLanes = kNv ? 2 : 4;
   const float g = kNv && tscale ? *tscale : 1.f;
+  const float inv6g = 1.f / (6.f * g);
   const long long limit = rows_in_use(rows_dev, rows) * sp.per_row;
   const long long g0 = (long long)blockIdx.x * (kThreads * kUnroll) + threadIdx.x;
-  float v[kUnroll][8], u[kUnroll][8];
+  Eight<T> v[kUnroll], u[kSwiglu ? kUnroll : 1];
 #pragma unroll
   for (int i = 0; i < kUnroll; ++i) {
     const long long n = g0 + i * kThreads;
-#pragma unroll
-    for (int q = 0; q < 8; ++q) v[i][q] = u[i][q] = 0.f;
-    if (n >= limit) continue;
-    long long row;
-    uint32_t c;
-    if (kSwiglu) {
+    if (n >= limit) {
+      v[i] = {};
+      if (kSwiglu) u[i] = {};
+    } else if (kSwiglu) {
+      long long row;
+      uint32_t c;
       split_at(sp, n, &row, &c);
       const T* p = x + row * 2 * (8LL * sp.per_row) + 8LL * c;
-      load8(p, v[i]);
-      load8(p + 8LL * sp.per_row, u[i]);
+      v[i].load(p);
+      u[i].load(p + 8LL * sp.per_row);
     } else {
-      load8(x + n * 8, v[i]);
+      v[i].load(x + n * 8);
     }
   }
 #pragma unroll
   for (int i = 0; i < kUnroll; ++i) {
     const long long n = g0 + i * kThreads;
     uint32_t word, sc;
-    quantise8<T, kNv, kSwiglu>(v[i], u[i], g, &word, &sc);  // all lanes: it exchanges maxima
+    float a[8], b[8];
+    v[i].get(a);
+    u[kSwiglu ? i : 0].get(b);
+    quantise8<kNv, kSwiglu>(a, b, g, inv6g, &word, &sc);  // all lanes: it exchanges maxima
     if (n >= limit) continue;
     codes[n] = word;
     if (n % kLanes == 0) {
-      long long row;
-      uint32_t c;
-      split_at(sp, n, &row, &c);
-      uint8_t* d = scales + row * scale_stride + c / kLanes;
-      *d = uint8_t(sc);
-      if (c + kLanes == sp.per_row)  // the row's last block: zeros up to the stride
-        for (int b = int(c / kLanes) + 1; b < scale_stride; ++b) *++d = 0;
+      if (uint32_t(scale_stride) * kLanes == sp.per_row) {
+        scales[n / kLanes] = uint8_t(sc);
+      } else {
+        long long row;
+        uint32_t c;
+        split_at(sp, n, &row, &c);
+        uint8_t* d = scales + row * scale_stride + c / kLanes;
+        *d = uint8_t(sc);
+        if (c + kLanes == sp.per_row)  // the row's last block: zeros up to the stride
+          for (int b = int(c / kLanes) + 1; b < scale_stride; ++b) *++d = 0;
+      }
     }
   }
 }
 
-// 8 elements per thread: one word of codes, one scale byte (its block's other
+// 8 elements at a time: one word of codes, one scale byte (its block's other
 // lanes read the same), 16-byte stores.
-template <typename T, bool kNv>
+template <typename T, bool kNv, int kUnroll>
 __global__ void __launch_bounds__(kThreads)
 dequantize_kernel(const uint32_t* __restrict__ codes, const uint8_t* __restrict__ scales, long long rows, Split sp,
                   int scale_stride, const float* __restrict__ tscale, const int* __restrict__ rows_dev,
                   T* __restrict__ out) {
-  constexpr int kLanes = kNv ? 2 : 4, kVecs = sizeof(T) / 2;
+  constexpr int kLanes = kNv ? 2 : 4;
   const float g = kNv && tscale ? *tscale : 1.f;
   const long long limit = rows_in_use(rows_dev, rows) * sp.per_row;
-  const long long n = (long long)blockIdx.x * kThreads + threadIdx.x;
-  if (n >= limit) return;
-  long long row;
-  uint32_t c;
-  split_at(sp, n, &row, &c);
-  const uint32_t word = codes[n];
-  const float s = scale_value<kNv>(scales[row * scale_stride + c / kLanes]);
-  Vec<T, 8 / kVecs> o[kVecs];
+  const long long n0 = (long long)blockIdx.x * (kThreads * kUnroll) + threadIdx.x;
+  uint32_t word[kUnroll];
+  uint8_t sc[kUnroll];
 #pragma unroll
-  for (int i = 0; i < 8; i += 2) {
-    const __half2_raw q = __nv_cvt_fp4x2_to_halfraw2(__nv_fp4x2_storage_t(word >> (4 * i)), __NV_E2M1);
-    // code * s is exact; NV rounds once for g, then to T
-    o[i / (8 / kVecs)].v[i % (8 / kVecs)] = from_f32<T>(f16_to_f32(q.x) * s * g);
-    o[(i + 1) / (8 / kVecs)].v[(i + 1) % (8 / kVecs)] = from_f32<T>(f16_to_f32(q.y) * s * g);
+  for (int i = 0; i < kUnroll; ++i) {
+    const long long n = n0 + i * kThreads;
+    if (n >= limit) break;
+    word[i] = codes[n];
+    if (uint32_t(scale_stride) * kLanes == sp.per_row) {
+      sc[i] = scales[n / kLanes];
+    } else {
+      long long row;
+      uint32_t c;
+      split_at(sp, n, &row, &c);
+      sc[i] = scales[row * scale_stride + c / kLanes];
+    }
   }
 #pragma unroll
-  for (int i = 0; i < kVecs; ++i) reinterpret_cast<Vec<T, 8 / kVecs>*>(out + n * 8)[i] = o[i];
+  for (int i = 0; i < kUnroll; ++i) {
+    const long long n = n0 + i * kThreads;
+    if (n >= limit) break;
+    const float s = scale_value<kNv>(sc[i]);
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+      const __half2_raw q = __nv_cvt_fp4x2_to_halfraw2(__nv_fp4x2_storage_t(word[i] >> (4 * j)), __NV_E2M1);
+      // code * s is exact; NV rounds once for g, then to T
+      v[j] = f16_to_f32(q.x) * s;
+      v[j + 1] = f16_to_f32(q.y) * s;
+      if (kNv) {
+        v[j] *= g;
+        v[j + 1] *= g;
+      }
+    }
+    Eight<T> o;
+    o.set(v);
+    o.store(out + n * 8);
+  }
 }
 
 template <typename T, bool kNv, bool kSwiglu>
@@ -283,15 +372,20 @@ template <typename T>
 cudaError_t dequantize_as(bool nv, const void* codes, const uint8_t* scales, long long rows, int cols,
                           const float* tscale, const int* rows_dev, void* out, cudaStream_t st) {
   const Split sp = make_split(rows, cols / 8);
-  const unsigned grid = unsigned((sp.total + kThreads - 1) / kThreads);
-  if (nv)
-    dequantize_kernel<T, true><<<grid, kThreads, 0, st>>>(static_cast<const uint32_t*>(codes), scales, rows, sp,
-                                                         scale_stride(true, cols), tscale, rows_dev,
-                                                         static_cast<T*>(out));
+  const int stride = scale_stride(nv, cols);
+  const bool big = sp.total >= 148LL * 8 * kThreads * 4;  // as above
+  const int per = kThreads * (big ? 4 : 1);
+  const unsigned grid = unsigned((sp.total + per - 1) / per);
+  const uint32_t* c = static_cast<const uint32_t*>(codes);
+  T* o = static_cast<T*>(out);
+  if (nv && big)
+    dequantize_kernel<T, true, 4><<<grid, kThreads, 0, st>>>(c, scales, rows, sp, stride, tscale, rows_dev, o);
+  else if (nv)
+    dequantize_kernel<T, true, 1><<<grid, kThreads, 0, st>>>(c, scales, rows, sp, stride, tscale, rows_dev, o);
+  else if (big)
+    dequantize_kernel<T, false, 4><<<grid, kThreads, 0, st>>>(c, scales, rows, sp, stride, tscale, rows_dev, o);
   else
-    dequantize_kernel<T, false><<<grid, kThreads, 0, st>>>(static_cast<const uint32_t*>(codes), scales, rows, sp,
-                                                          scale_stride(false, cols), tscale, rows_dev,
-                                                          static_cast<T*>(out));
+    dequantize_kernel<T, false, 1><<<grid, kThreads, 0, st>>>(c, scales, rows, sp, stride, tscale, rows_dev, o);
   count_launches(1);
   return cudaGetLastError();
 }

@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "moe.h"
 #include "moe_common.cuh"
 #include "moe_internal.h"
@@ -45,10 +47,56 @@ __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2hal
 template <>
 __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 
-// N elements that are loaded and stored together.
+// N consecutive elements of type T that are loaded and stored together, held
+// as the words they are (16-bit elements taken apart only where they are used:
+// held one to a register they cost twice the registers, and the loads in
+// flight are what hides the latency).
 template <typename T, int N>
-struct alignas(sizeof(T) * N) Vec {
-  T v[N];
+struct alignas(sizeof(T) * N) Pack {
+  using Word = typename std::conditional<sizeof(T) * N == 2, uint16_t, uint32_t>::type;
+  static constexpr int kWords = int(sizeof(T) * N / sizeof(Word));
+  Word w[kWords];
+
+  __device__ __forceinline__ void get(float (&v)[N]) const {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = __uint_as_float(w[i]);
+    } else if constexpr (N == 1) {
+      v[0] = std::is_same<T, __half>::value ? f16_to_f32(w[0]) : bf16_to_f32(w[0]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) {
+        if constexpr (std::is_same<T, __half>::value) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+          v[2 * i] = f.x;
+          v[2 * i + 1] = f.y;
+        } else {
+          v[2 * i] = __uint_as_float(uint32_t(w[i]) << 16);
+          v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void set(const float (&v)[N]) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) w[i] = __float_as_uint(v[i]);
+    } else if constexpr (N == 1) {
+      const T t = from_f32<T>(v[0]);
+      w[0] = *reinterpret_cast<const uint16_t*>(&t);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) {
+        if constexpr (std::is_same<T, __half>::value) {
+          const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+          w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        } else {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+          w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+      }
+    }
+  }
 };
 
 }  // namespace moe

@@ -26,97 +26,131 @@ __device__ __forceinline__ int pair_row(const int* __restrict__ inv, long long p
 }
 
 // A block has kWarps warps: `wpt` (a power of two) of them take consecutive
-// 32-vector segments of one token's row, so kWarps / wpt tokens per block;
+// segments of one token's row, so kWarps / wpt tokens per block;
 // gridDim.y blocks share the segments of long rows.
 struct TokenSplit {
-  int wpt;
-  int tokens() const { return kWarps / wpt; }
-  dim3 grid(int T, int nvec) const {
-    const int nseg = (nvec + 31) / 32;
-    int y = (nseg + wpt - 1) / wpt;
-    if (y > 65535) y = 65535;
-    return dim3(unsigned((T + tokens() - 1) / tokens()), unsigned(y));
+  int wpt, nseg;
+  dim3 grid(int T) const {
+    const int tokens = kWarps / wpt, y = (nseg + wpt - 1) / wpt;
+    return dim3(unsigned((T + tokens - 1) / tokens), unsigned(y < 65535 ? y : 65535));
   }
 };
-TokenSplit token_split(int nvec) {
-  const int nseg = (nvec + 31) / 32;
+TokenSplit token_split(int nvec, int seg) {
+  const int nseg = (nvec + seg - 1) / seg;
   int w = 1;
   while (w < kWarps && w < nseg) w *= 2;
-  return {w};
+  return {w, nseg};
 }
 
-// One warp: 32 vectors of a token's row are read once and written to the
+// Vectors that a lane takes of a segment: narrow ones (rows that are not
+// 16-byte aligned) in fours, to keep as many bytes in flight.
+template <typename V>
+constexpr int lane_vecs() { return sizeof(V) >= 8 ? 1 : 4; }
+
+// One warp: a segment of a token's row is read once and written to the
 // token's k rows.
 template <typename V>
 __global__ void __launch_bounds__(kWarps * 32)
 permute_kernel(const V* __restrict__ x, const int* __restrict__ inv, int T, int k, int nvec, int wpt,
                V* __restrict__ xp, WsHeader* hdr) {
+  constexpr int kU = lane_vecs<V>(), kSeg = 32 * kU;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int t = blockIdx.x * (kWarps / wpt) + warp / wpt;
   if (t >= T) return;
   const long long p0 = (long long)t * k, nrows = (long long)T * k;
-  for (int s = blockIdx.y * wpt + warp % wpt; s < (nvec + 31) / 32; s += gridDim.y * wpt) {
-    const int c = s * 32 + lane;
-    V v{};
-    if (c < nvec) v = x[(size_t)t * nvec + c];
+  for (int s = blockIdx.y * wpt + warp % wpt; s < (nvec + kSeg - 1) / kSeg; s += gridDim.y * wpt) {
+    const int c = s * kSeg + lane;
+    V v[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) v[u] = x[(size_t)t * nvec + min(c + 32 * u, nvec - 1)];
     for (int j0 = 0; j0 < k; j0 += 32) {
       const int mine = j0 + lane < k ? pair_row(inv, p0 + j0 + lane, nrows, hdr) : -1;
       const int n = min(32, k - j0);
       for (int j = 0; j < n; ++j) {
         const int r = __shfl_sync(0xffffffffu, mine, j);
-        if (r >= 0 && c < nvec) xp[(size_t)r * nvec + c] = v;
+        if (r < 0) continue;
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+          if (c + 32 * u < nvec) xp[(size_t)r * nvec + c + 32 * u] = v[u];
       }
     }
   }
 }
 
-// One warp: 32 vectors of out[t]; the rows of up to kBatch pairs are in
-// flight at a time.
+// Adds kB rows, all loads first. Rows of -1 are left out and not read.
+template <typename T, int N, int kU, int kB, bool kWeighted>
+__device__ __forceinline__ void add_rows(const Pack<T, N>* __restrict__ y, int mine, float wmine, int j, int nvec,
+                                         const int (&c)[kU], float (&acc)[kU][N]) {
+  int row[kB];
+  bool all = true;
+#pragma unroll
+  for (int b = 0; b < kB; ++b) {
+    row[b] = __shfl_sync(0xffffffffu, mine, j + b);
+    all = all && row[b] >= 0;
+  }
+  Pack<T, N> v[kB][kU];
+  if (all) {
+#pragma unroll
+    for (int b = 0; b < kB; ++b)
+#pragma unroll
+      for (int u = 0; u < kU; ++u) v[b][u] = y[(size_t)row[b] * nvec + c[u]];
+  } else {
+#pragma unroll
+    for (int b = 0; b < kB; ++b)
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+        if (row[b] >= 0) v[b][u] = y[(size_t)row[b] * nvec + c[u]];
+  }
+#pragma unroll
+  for (int b = 0; b < kB; ++b) {
+    const float w = kWeighted ? __shfl_sync(0xffffffffu, wmine, j + b) : 1.f;
+    if (all || row[b] >= 0) {
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        float x[N];
+        v[b][u].get(x);
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[u][i] = kWeighted ? fmaf(w, x[i], acc[u][i]) : acc[u][i] + x[i];
+      }
+    }
+  }
+}
+
+// One warp: a segment of out[t], the rows of several pairs in flight.
 template <typename T, int N, bool kWeighted>
-__global__ void __launch_bounds__(kWarps * 32)
-unpermute_kernel(const Vec<T, N>* __restrict__ y, const int* __restrict__ inv, const float* __restrict__ w, int tokens,
-                 int k, int nvec, int wpt, Vec<T, N>* __restrict__ out, WsHeader* hdr) {
-  constexpr int kBatch = 8;
+__global__ void __launch_bounds__(kWarps * 32, 4)
+unpermute_kernel(const Pack<T, N>* __restrict__ y, const int* __restrict__ inv, const float* __restrict__ w, int tokens,
+                 int k, int nvec, int wpt, Pack<T, N>* __restrict__ out, WsHeader* hdr) {
+  constexpr int kU = lane_vecs<Pack<T, N>>(), kSeg = 32 * kU;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int t = blockIdx.x * (kWarps / wpt) + warp / wpt;
   if (t >= tokens) return;
   const long long p0 = (long long)t * k, nrows = (long long)tokens * k;
-  for (int s = blockIdx.y * wpt + warp % wpt; s < (nvec + 31) / 32; s += gridDim.y * wpt) {
-    const int c = s * 32 + lane;
-    float acc[N];
+  for (int s = blockIdx.y * wpt + warp % wpt; s < (nvec + kSeg - 1) / kSeg; s += gridDim.y * wpt) {
+    int c[kU];  // lanes behind the row's end read its last vector again
+    float acc[kU][N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) acc[i] = 0.f;
+    for (int u = 0; u < kU; ++u) {
+      c[u] = min(s * kSeg + 32 * u + lane, nvec - 1);
+#pragma unroll
+      for (int i = 0; i < N; ++i) acc[u][i] = 0.f;
+    }
     for (int j0 = 0; j0 < k; j0 += 32) {
       const bool has = j0 + lane < k;
       const int mine = has ? pair_row(inv, p0 + j0 + lane, nrows, hdr) : -1;
-      float wmine = 1.f;
-      if (kWeighted && has) wmine = w[p0 + j0 + lane];
+      float wm = 1.f;
+      if (kWeighted && has) wm = w[p0 + j0 + lane];
       const int n = min(32, k - j0);
-      for (int j1 = 0; j1 < n; j1 += kBatch) {
-        Vec<T, N> v[kBatch];
-        int row[kBatch];
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-          row[j] = __shfl_sync(0xffffffffu, mine, (j1 + j) & 31);
-          if (j1 + j >= n) row[j] = -1;
-          if (row[j] >= 0 && c < nvec) v[j] = y[(size_t)row[j] * nvec + c];
-        }
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-          const float wj = kWeighted ? __shfl_sync(0xffffffffu, wmine, (j1 + j) & 31) : 1.f;
-          if (row[j] >= 0 && c < nvec) {
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-              acc[i] = kWeighted ? fmaf(wj, to_f32(v[j].v[i]), acc[i]) : acc[i] + to_f32(v[j].v[i]);
-          }
-        }
-      }
+      int j = 0;
+      for (; j + 5 <= n; j += 5) add_rows<T, N, kU, 5, kWeighted>(y, mine, wm, j, nvec, c, acc);
+      for (; j + 2 <= n; j += 2) add_rows<T, N, kU, 2, kWeighted>(y, mine, wm, j, nvec, c, acc);
+      if (j < n) add_rows<T, N, kU, 1, kWeighted>(y, mine, wm, j, nvec, c, acc);
     }
-    if (c < nvec) {
-      Vec<T, N> o;
 #pragma unroll
-      for (int i = 0; i < N; ++i) o.v[i] = from_f32<T>(acc[i]);
-      out[(size_t)t * nvec + c] = o;
+    for (int u = 0; u < kU; ++u) {
+      Pack<T, N> o;
+      o.set(acc[u]);
+      if (s * kSeg + 32 * u + lane < nvec) out[(size_t)t * nvec + c[u]] = o;
     }
   }
 }
@@ -126,9 +160,9 @@ unpermute_kernel(const Vec<T, N>* __restrict__ y, const int* __restrict__ inv, c
 // for all but a token's first pair).
 template <typename T, int N, int kPW>
 __global__ void __launch_bounds__(kWarps * 32)
-unpermute_grad_kernel(const Vec<T, N>* __restrict__ dout, const Vec<T, N>* __restrict__ y,
+unpermute_grad_kernel(const Pack<T, N>* __restrict__ dout, const Pack<T, N>* __restrict__ y,
                       const int* __restrict__ inv, const float* __restrict__ w, long long pairs, int k, int nvec,
-                      Vec<T, N>* __restrict__ dy, float* __restrict__ dw, WsHeader* hdr) {
+                      Pack<T, N>* __restrict__ dy, float* __restrict__ dw, WsHeader* hdr) {
   constexpr int kUnroll = kPW > 1 ? 1 : N * sizeof(T) == 16 ? 4 : 8;
   __shared__ float part[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -138,11 +172,11 @@ unpermute_grad_kernel(const Vec<T, N>* __restrict__ dout, const Vec<T, N>* __res
     const int r = pair_row(inv, p, pairs, hdr);
     if (r >= 0) {
       const float wp = w[p];
-      const Vec<T, N>* d = dout + (size_t)(p / k) * nvec;
-      const Vec<T, N>* yr = y + (size_t)r * nvec;
-      Vec<T, N>* o = dy + (size_t)r * nvec;
+      const Pack<T, N>* d = dout + (size_t)(p / k) * nvec;
+      const Pack<T, N>* yr = y + (size_t)r * nvec;
+      Pack<T, N>* o = dy + (size_t)r * nvec;
       for (int c0 = (warp % kPW) * 32 * kUnroll; c0 < nvec; c0 += kPW * 32 * kUnroll) {
-        Vec<T, N> a[kUnroll], b[kUnroll];
+        Pack<T, N> a[kUnroll], b[kUnroll];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
           const int c = c0 + u * 32 + lane;
@@ -155,13 +189,16 @@ unpermute_grad_kernel(const Vec<T, N>* __restrict__ dout, const Vec<T, N>* __res
         for (int u = 0; u < kUnroll; ++u) {
           const int c = c0 + u * 32 + lane;
           if (c < nvec) {
-            Vec<T, N> g;
+            float x[N], z[N];
+            a[u].get(x);
+            b[u].get(z);
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-              const float x = to_f32(a[u].v[i]);
-              sum = fmaf(x, to_f32(b[u].v[i]), sum);
-              g.v[i] = from_f32<T>(wp * x);
+              sum = fmaf(x[i], z[i], sum);
+              x[i] *= wp;
             }
+            Pack<T, N> g;
+            g.set(x);
             o[c] = g;
           }
         }
@@ -199,8 +236,8 @@ template <typename V>
 cudaError_t run_permute(const void* x, const int* inv, int T, int k, size_t row_bytes, void* xp, WsHeader* hdr,
                         cudaStream_t st) {
   const int nvec = int(row_bytes / sizeof(V));
-  const TokenSplit s = token_split(nvec);
-  permute_kernel<V><<<s.grid(T, nvec), kWarps * 32, 0, st>>>(static_cast<const V*>(x), inv, T, k, nvec, s.wpt,
+  const TokenSplit s = token_split(nvec, 32 * lane_vecs<V>());
+  permute_kernel<V><<<s.grid(T), kWarps * 32, 0, st>>>(static_cast<const V*>(x), inv, T, k, nvec, s.wpt,
                                                             static_cast<V*>(xp), hdr);
   return done();
 }
@@ -208,14 +245,14 @@ cudaError_t run_permute(const void* x, const int* inv, int T, int k, size_t row_
 template <typename T, int N>
 cudaError_t run_unpermute(const void* y, const int* inv, const float* w, int tokens, int k, int H, void* out,
                           WsHeader* hdr, cudaStream_t st) {
-  using V = Vec<T, N>;
+  using V = Pack<T, N>;
   const int nvec = H / N;
-  const TokenSplit s = token_split(nvec);
+  const TokenSplit s = token_split(nvec, 32 * lane_vecs<V>());
   if (w)
-    unpermute_kernel<T, N, true><<<s.grid(tokens, nvec), kWarps * 32, 0, st>>>(
+    unpermute_kernel<T, N, true><<<s.grid(tokens), kWarps * 32, 0, st>>>(
         static_cast<const V*>(y), inv, w, tokens, k, nvec, s.wpt, static_cast<V*>(out), hdr);
   else
-    unpermute_kernel<T, N, false><<<s.grid(tokens, nvec), kWarps * 32, 0, st>>>(
+    unpermute_kernel<T, N, false><<<s.grid(tokens), kWarps * 32, 0, st>>>(
         static_cast<const V*>(y), inv, nullptr, tokens, k, nvec, s.wpt, static_cast<V*>(out), hdr);
   return done();
 }
@@ -223,7 +260,7 @@ cudaError_t run_unpermute(const void* y, const int* inv, const float* w, int tok
 template <typename T, int N>
 cudaError_t run_unpermute_grad(const void* dout, const void* y, const int* inv, const float* w, int tokens, int k,
                                int H, void* dy, float* dw, WsHeader* hdr, cudaStream_t st) {
-  using V = Vec<T, N>;
+  using V = Pack<T, N>;
   const long long pairs = (long long)tokens * k;
   // few pairs: a block per pair, so that a row is read by eight warps at once
   if (pairs < 1184)
