@@ -104,9 +104,7 @@ struct Eight {
   }
 };
 
-// Kept out of line: rarely called, and its registers would halve the warps in
-// flight of the common path.
-__device__ __noinline__ double swiglu_f64(float gate, float up) {
+__device__ __forceinline__ double swiglu_f64(float gate, float up) {
   return double(gate) / (1.0 + exp(-double(gate))) * double(up);
 }
 __device__ __forceinline__ float ex2_approx(float x) {
@@ -138,47 +136,122 @@ __device__ __forceinline__ float beside(float border, double diff) {
 __device__ __forceinline__ uint32_t e2m1x2(float low, float high) {
   return __nv_cvt_float2_to_fp4x2(make_float2(low, high), __NV_E2M1, cudaRoundNearest);
 }
+// Codes of 8 values times f, the first in the low nibble. One instruction
+// sequence, so that the conversions place their bytes themselves.
 __device__ __forceinline__ uint32_t e2m1_word(const float (&h)[8], float f) {
-  return e2m1x2(h[0] * f, h[1] * f) | e2m1x2(h[2] * f, h[3] * f) << 8 | e2m1x2(h[4] * f, h[5] * f) << 16 |
-         e2m1x2(h[6] * f, h[7] * f) << 24;
+  uint32_t w;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(w)
+      : "f"(h[0] * f), "f"(h[1] * f), "f"(h[2] * f), "f"(h[3] * f), "f"(h[4] * f), "f"(h[5] * f), "f"(h[6] * f),
+        "f"(h[7] * f));
+  return w;
+}
+// Largest magnitude of 8 elements, NaN if one of them is. Without their signs
+// the bits of 16-bit floats order like the values, NaN above infinity: two at a
+// time by integer maxima.
+template <typename T>
+__device__ __forceinline__ float abs_max(const Eight<T>& v) {
+  if constexpr (sizeof(T) == 2) {
+    uint32_t m = v.p[0].w[0] & 0x7fff7fffu;
+#pragma unroll
+    for (int i = 1; i < 4; ++i) m = __vmaxu2(m, v.p[0].w[i] & 0x7fff7fffu);
+    const uint16_t b = uint16_t(max(m & 0xffffu, m >> 16));
+    return std::is_same<T, __half>::value ? f16_to_f32(b) : bf16_to_f32(b);
+  } else {
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max_nan(m, fabsf(__uint_as_float(v.p[i / 4].w[i % 4])));
+    return m;
+  }
 }
 
-// Codes and the scale byte of one block whose lanes hold 8 elements each.
-// g: the tensor scale, inv6g about 1 / (6 g).
-template <bool kNv, bool kSwiglu>
-__device__ __forceinline__ void quantise8(const float (&x)[8], const float (&up)[8], float g, float inv6g,
-                                          uint32_t* codes, uint32_t* scale) {
+// The rare exact decisions read the 8 elements again (`up` of SwiGLU inputs
+// is up_at elements behind): out of line and from memory, they cost the common
+// path neither registers nor instruction cache.
+template <typename T, bool kSwiglu>
+__device__ __noinline__ double exact_top(const T* x, long long up_at) {
+  Eight<T> v, u;
+  v.load(x);
+  u.load(x + up_at);
+  float a[8], b[8];
+  v.get(a);
+  u.get(b);
+  double t = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) t = fmax(t, fabs(kSwiglu ? swiglu_f64(a[i], b[i]) : double(a[i])));
+  return t;
+}
+// `word` with the codes that `differ` has bits in decided exactly; scale = s g,
+// inv about its reciprocal.
+template <typename T, bool kSwiglu>
+__device__ __noinline__ uint32_t exact_codes(const T* x, long long up_at, float s, float g, float inv, uint32_t word,
+                                             uint32_t differ) {
+  Eight<T> v, u;
+  v.load(x);
+  u.load(x + up_at);
+  float a[8], b[8];
+  v.get(a);
+  u.get(b);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (differ >> (4 * i) & 15u) {
+      const double h = kSwiglu ? swiglu_f64(a[i], b[i]) : double(a[i]);
+      // borders between E2M1 values have 2 mantissa bits; border * s * g is exact in 64 bits
+      const float border = border_of(fabsf(float(h)) * inv, 2);
+      const float q = beside(border, fabs(h) - double(border) * double(s) * double(g));
+      word = (word & ~(15u << (4 * i))) | (e2m1x2(copysignf(q, float(h)), 0.f) & 15u) << (4 * i);
+    }
+  }
+  return word;
+}
+
+// Codes and the scale byte of one block whose lanes hold 8 elements each, read
+// from x (lanes that read none, `has` false, hold zeros). g: the tensor scale,
+// inv6g about 1 / (6 g).
+template <typename T, bool kNv, bool kSwiglu>
+__device__ __forceinline__ void quantise8(const Eight<T>& v, const Eight<T>& u, const T* x, long long up_at, bool has,
+                                          float g, float inv6g, uint32_t* codes, uint32_t* scale) {
   constexpr int kLanes = kNv ? 2 : 4;
   constexpr float kOff = kSwiglu ? kOffSwiglu : kOffPlain;
   float h[8];
-  float top = 0.f, exps = 0.f;
+  float top = 0.f;
+  v.get(h);
+  if (kSwiglu) {
+    float up[8], exps = 0.f;
+    u.get(up);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (kSwiglu) {
-      const float e = ex2_approx(x[i] * -1.4426950408889634f);
-      h[i] = x[i] * rcp_approx(1.f + e) * up[i];
+    for (int i = 0; i < 8; ++i) {
+      const float e = ex2_approx(h[i] * -1.4426950408889634f);
+      h[i] = h[i] * rcp_approx(1.f + e) * up[i];
       exps += e;
-    } else {
-      h[i] = x[i];
+    }
+    if (!(exps < kExpSum)) {
+      v.get(h);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[i] = float(h[i] < -80.f ? double(h[i]) * exp(double(h[i])) * double(up[i])
+                                                            : swiglu_f64(h[i], up[i]));
     }
   }
   if (kSwiglu) {
-    if (!(exps < kExpSum)) {
+    uint32_t m = 0;  // as integers: max takes the magnitude of one operand for free only where it need not keep NaN
 #pragma unroll
-      for (int i = 0; i < 8; ++i) h[i] = float(swiglu_f64(x[i], up[i]));
-    }
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(h[i]) & 0x7fffffffu);
+    top = __uint_as_float(m);
+  } else {
+    top = abs_max<T>(v);
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) top = max_nan(top, fabsf(h[i]));
 #pragma unroll
   for (int o = 1; o < kLanes; o *= 2) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
   const bool bad = !(top <= 3.402823466e38f);  // infinite or NaN
 
   // largest |h| in 64 bits, for the rare border cases of the scale
   auto top_f64 = [&]() {
-    double t = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) t = fmax(t, fabs(kSwiglu ? swiglu_f64(x[i], up[i]) : double(h[i])));
+    double t = has ? exact_top<T, kSwiglu>(x, up_at) : 0.0;
 #pragma unroll
     for (int o = 1; o < kLanes; o *= 2) t = fmax(t, __shfl_xor_sync(0xffffffffu, t, o));
     return t;
@@ -210,81 +283,78 @@ __device__ __forceinline__ void quantise8(const float (&x)[8], const float (&up)
         if (near) top = t < double(__uint_as_float(above)) ? __uint_as_float(above - 1) : __uint_as_float(above);
       }
     }
-    const int e = int(__float_as_uint(top) >> 23) - 2;  // biased floor(log2), less E2M1's largest exponent
-    *scale = bad ? 0xffu : uint32_t(max(e, 0));
-    s = 1.f;
-    inv = __uint_as_float(uint32_t(254 - max(e, 0)) << 23);
+    const int e = max(int(__float_as_uint(top) >> 23) - 2, 0);  // biased floor(log2), less E2M1's largest exponent
+    *scale = bad ? 0xffu : uint32_t(e);
+    s = e ? __uint_as_float(uint32_t(e) << 23) : 0x1p-127f;
+    inv = __uint_as_float(uint32_t(254 - e) << 23);
   }
 
   uint32_t word = e2m1_word(h, kNv || kSwiglu ? inv * (1.f - kOff) : inv);
   if (kNv || kSwiglu) {
     // a code that the uncertainty of its quotient could change is decided exactly
     const uint32_t differ = word ^ e2m1_word(h, inv * (1.f + kOff));
-    if (differ) {
-      const double unit = kNv ? double(s) * double(g) : 1.0 / double(inv);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (differ >> (4 * i) & 15u) {
-          const float border = border_of(fabsf(h[i]) * inv, 2);  // these borders have 2 mantissa bits
-          const float v = kSwiglu ? beside(border, fabs(swiglu_f64(x[i], up[i])) - double(border) * unit)
-                                  : beside(border, fmaf(-(border * s), g, fabsf(h[i])));
-          word = (word & ~(15u << (4 * i))) | (e2m1x2(copysignf(v, h[i]), 0.f) & 15u) << (4 * i);
-        }
-      }
-    }
+    if (differ && has) word = exact_codes<T, kSwiglu>(x, up_at, s, g, inv, word, differ);
   }
   *codes = bad || (kNv && s == 0.f) ? 0u : word;
 }
 
+// How warps share the chunks of 8 elements: 2^lg lanes side by side on a row
+// (32 >> lg rows per warp), each lane with up to kUnroll chunks 2^lg apart;
+// `parts` warps make a row.
+struct WarpSplit {
+  int per_row, lg;
+  uint32_t parts;
+  long long warps;
+};
+WarpSplit warp_split(long long rows, int per_row, int unroll) {
+  // as many lanes on a row as keep 9 of 10 busy; 4 lanes (a block) always do
+  int lg = 5;
+  while (lg > 2 && 10 * per_row < 9 * (((per_row + (1 << lg) - 1) >> lg) << lg)) --lg;
+  const uint32_t parts = uint32_t((per_row + (unroll << lg) - 1) / (unroll << lg));
+  return {per_row, lg, parts, (rows + (32 >> lg) - 1) / (32 >> lg) * parts};
+}
+
 template <typename T, bool kNv, bool kSwiglu, int kUnroll>
 __global__ void __launch_bounds__(kThreads, 4)
-quantize_kernel(const T* __restrict__ x, long long rows, Split sp, int scale_stride, const float* __restrict__ tscale,
-                const int* __restrict__ rows_dev, uint32_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+quantize_kernel(const T* __restrict__ x, long long rows, WarpSplit ws, int scale_stride,
+                const float* __restrict__ tscale, const int* __restrict__ rows_dev, uint32_t* __restrict__ codes,
+                uint8_t* __restrict__ scales) {
   constexpr int kLanes = kNv ? 2 : 4;
   const float g = kNv && tscale ? *tscale : 1.f;
   const float inv6g = 1.f / (6.f * g);
-  const long long limit = rows_in_use(rows_dev, rows) * sp.per_row;
-  const long long g0 = (long long)blockIdx.x * (kThreads * kUnroll) + threadIdx.x;
+  const uint32_t warp = blockIdx.x * (kThreads / 32) + threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t group = warp / ws.parts;
+  const long long row = (long long)group * (32 >> ws.lg) + (lane >> ws.lg);
+  const int step = 1 << ws.lg;
+  const int c0 = int((warp - group * ws.parts) * kUnroll << ws.lg) + int(lane & (step - 1));
+  const int end = row < rows_in_use(rows_dev, rows) ? ws.per_row : 0;  // chunks of this lane's row
+  x += (row * (kSwiglu ? 2 : 1) * ws.per_row + c0) * 8;
+  codes += row * ws.per_row + c0;
+  scales += row * scale_stride + c0 / kLanes;
   Eight<T> v[kUnroll], u[kSwiglu ? kUnroll : 1];
 #pragma unroll
   for (int i = 0; i < kUnroll; ++i) {
-    const long long n = g0 + i * kThreads;
-    if (n >= limit) {
-      v[i] = {};
-      if (kSwiglu) u[i] = {};
-    } else if (kSwiglu) {
-      long long row;
-      uint32_t c;
-      split_at(sp, n, &row, &c);
-      const T* p = x + row * 2 * (8LL * sp.per_row) + 8LL * c;
-      v[i].load(p);
-      u[i].load(p + 8LL * sp.per_row);
-    } else {
-      v[i].load(x + n * 8);
+    v[i] = {};
+    if (kSwiglu) u[i] = {};
+    if (c0 + i * step < end) {
+      v[i].load(x + i * step * 8);
+      if (kSwiglu) u[i].load(x + (i * step + ws.per_row) * 8LL);
     }
   }
 #pragma unroll
   for (int i = 0; i < kUnroll; ++i) {
-    const long long n = g0 + i * kThreads;
     uint32_t word, sc;
-    float a[8], b[8];
-    v[i].get(a);
-    u[kSwiglu ? i : 0].get(b);
-    quantise8<kNv, kSwiglu>(a, b, g, inv6g, &word, &sc);  // all lanes: it exchanges maxima
-    if (n >= limit) continue;
-    codes[n] = word;
-    if (n % kLanes == 0) {
-      if (uint32_t(scale_stride) * kLanes == sp.per_row) {
-        scales[n / kLanes] = uint8_t(sc);
-      } else {
-        long long row;
-        uint32_t c;
-        split_at(sp, n, &row, &c);
-        uint8_t* d = scales + row * scale_stride + c / kLanes;
-        *d = uint8_t(sc);
-        if (c + kLanes == sp.per_row)  // the row's last block: zeros up to the stride
-          for (int b = int(c / kLanes) + 1; b < scale_stride; ++b) *++d = 0;
-      }
+    const int c = c0 + i * step;
+    // all lanes: it exchanges maxima
+    quantise8<T, kNv, kSwiglu>(v[i], u[kSwiglu ? i : 0], x + i * step * 8, kSwiglu ? ws.per_row * 8LL : 0, c < end, g,
+                               inv6g, &word, &sc);
+    if (c >= end) continue;
+    codes[i * step] = word;
+    if (c % kLanes == 0) {
+      uint8_t* d = scales + i * step / kLanes;
+      *d = uint8_t(sc);
+      if (c + kLanes == end)  // the row's last block: zeros up to the stride
+        for (int k = c / kLanes + 1; k < scale_stride; ++k) *++d = 0;
     }
   }
 }
@@ -342,17 +412,26 @@ dequantize_kernel(const uint32_t* __restrict__ codes, const uint8_t* __restrict_
 template <typename T, bool kNv, bool kSwiglu>
 cudaError_t run_quantize(const void* x, long long rows, int cols, const float* tscale, const int* rows_dev,
                          void* codes, uint8_t* scales, cudaStream_t st) {
-  const Split sp = make_split(rows, cols / 8);
-  const int stride = scale_stride(kNv, cols);
-  // four chunks per thread keep enough loads in flight once the grid fills the GPU; small inputs spread wider
+  // Several chunks per lane keep enough loads in flight once the grid fills
+  // the GPU; small inputs spread wider. Lanes behind a row's end compute all
+  // the same, so three chunks where they leave fewer of those (rows of 96
+  // chunks, SwiGLU: 66 us in threes, 87 in twos).
   constexpr int kUnroll = sizeof(T) == 4 || kSwiglu ? 2 : 4;
-  if (sp.total >= 148LL * 8 * kThreads * kUnroll) {
-    const long long grid = (sp.total + kThreads * kUnroll - 1) / (kThreads * kUnroll);
-    quantize_kernel<T, kNv, kSwiglu, kUnroll><<<unsigned(grid), kThreads, 0, st>>>(
-        static_cast<const T*>(x), rows, sp, stride, tscale, rows_dev, static_cast<uint32_t*>(codes), scales);
+  const T* in = static_cast<const T*>(x);
+  uint32_t* out = static_cast<uint32_t*>(codes);
+  const int stride = scale_stride(kNv, cols), per_row = cols / 8;
+  auto launch = [&](auto kernel, const WarpSplit& ws) {
+    const unsigned grid = unsigned((ws.warps + kThreads / 32 - 1) / (kThreads / 32));
+    kernel<<<grid, kThreads, 0, st>>>(in, rows, ws, stride, tscale, rows_dev, out, scales);
+  };
+  if (rows * per_row < 148LL * 8 * kThreads * kUnroll) {
+    launch(quantize_kernel<T, kNv, kSwiglu, 1>, warp_split(rows, per_row, 1));
   } else {
-    quantize_kernel<T, kNv, kSwiglu, 1><<<unsigned((sp.total + kThreads - 1) / kThreads), kThreads, 0, st>>>(
-        static_cast<const T*>(x), rows, sp, stride, tscale, rows_dev, static_cast<uint32_t*>(codes), scales);
+    const WarpSplit a = warp_split(rows, per_row, kUnroll), b = warp_split(rows, per_row, 3);
+    if (a.parts * kUnroll <= b.parts * 3)
+      launch(quantize_kernel<T, kNv, kSwiglu, kUnroll>, a);
+    else
+      launch(quantize_kernel<T, kNv, kSwiglu, 3>, b);
   }
   count_launches(1);
   return cudaGetLastError();
