@@ -7,20 +7,22 @@
 // the MMA (kind::mxf4 for MX, kind::mxf4nvf4 for NV); products are exact and
 // sums stay in fp32 in TMEM until the one rounding of the epilogue.
 //
-// One persistent CTA per SM, 20 warps:
+// One persistent CTA per SM, 16 warps:
 //   warp 0       codes: TMA tiles of 128 bytes (256 elements of K) per row,
 //                128-byte swizzle, kStages deep
-//   warp 1       MMA issuer, four K = 64 MMAs per stage
+//   warp 1       MMA issuer: the scale words of 16 bytes of each row from
+//                shared memory to TMEM (tcgen05.cp, in the MMAs' own queue), then
+//                four K = 64 MMAs per stage
 //   warp 2       scales: TMA tiles of 32 bytes per row, kSlots deep
-//   warps 4-11   scale words from shared memory into TMEM, where the MMA reads
-//                them: lane (row % 32), column (row / 32), the same in all four
-//                lane quarters, so that each warp fills its own; two groups
-//                of four take turns. They are
-//                written from registers because the rows' words are 4 bytes
-//                of a row-major matrix, which no copy into TMEM can gather; on
-//                the way the bytes behind K become 0
-//   warps 12-19  epilogue: TMEM -> registers -> smem (transposed) -> global,
+//   warps 4-6    scales, in place: row-major 32-byte rows become the blocks
+//                tcgen05.cp wants, 4 bytes of each of 128 rows together (the
+//                weights' rows, the first and the second 128 tokens); what
+//                lies behind K becomes 0
+//   warps 8-15   epilogue: TMEM -> registers -> smem (transposed) -> global,
 //                on the other of two accumulators
+// The scale words could go straight to TMEM from the warps' registers, but
+// those stores and the MMAs get in each other's way: 8192^3 MX 326 us, with
+// tcgen05.cp SPEED_CP us (the MMAs alone take 141).
 //
 // Tiles: every CTA sums up the experts' token tiles (offsets are on the
 // device) and takes tiles b, b + grid, ... of the list "expert, token tile, 128
@@ -43,27 +45,23 @@ namespace {
 constexpr int kBM = 128;       // weight rows per tile
 constexpr int kBKBytes = 128;  // code bytes of a row per stage: 256 elements
 constexpr int kBoxRows = 32;   // token rows per TMA box
-constexpr int kThreads = 640;
-constexpr int kEpiWarps = 8, kScaleWarps = 8;
+constexpr int kThreads = 512;
+constexpr int kEpiWarps = 8, kScaleWarps = 3;
 constexpr int kSlotRow = 32;   // scale bytes of a row per slot
 constexpr int kSlots = 3;
-#ifndef PF
-#define PF 8
-#endif
-constexpr int kPrefetch = PF;
 constexpr int kListed = 256;  // tiles listed at a time
 constexpr int kScratch = 2048;  // epilogue staging per warp: 32 weight rows of 32 (16 bits) or 16 tokens
 
 // kTN: tokens per tile (a multiple of 32); kStages: ring depth.
 template <int kTN, int kStages>
 struct Cfg {
-  static constexpr int kBBlocks = (kTN + 31) / 32;  // 32-row blocks of the token side
+  static constexpr int kHalves = (kTN + 127) / 128;  // 128-row scale blocks of the token side
   static constexpr int kABytes = kBM * kBKBytes;
   static constexpr int kStageBytes = kABytes + kTN * kBKBytes;
-  static constexpr int kSlotBytes = (kBM + kTN) * kSlotRow;
+  static constexpr int kSlotBytes = 128 * (1 + kHalves) * kSlotRow;
   // TMEM: two accumulators of kTN columns, then buffers of the scale words of
   // 16 bytes of each row: 4 x 4 columns of weights, 4 x kBCols of tokens
-  static constexpr int kBCols = kBBlocks > 4 ? 8 : 4;
+  static constexpr int kBCols = 4 * kHalves;
   static constexpr int kSfCols = 4 * (4 + kBCols);
   static constexpr int kSfBufs = (512 - 2 * kTN) / kSfCols >= 4 ? 4 : 2;
   static constexpr int kCols = 2 * kTN + kSfBufs * kSfCols;
@@ -103,8 +101,8 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ __align__(8) uint64_t full_bar[kStages], empty_bar[kStages];      // codes
-  __shared__ __align__(8) uint64_t sfull_bar[kSlots], sempty_bar[kSlots];      // scales in shared memory
-  __shared__ __align__(8) uint64_t wfull_bar[C::kSfBufs], wempty_bar[C::kSfBufs];  // scale words in TMEM
+  // scales in shared memory: arrived, in blocks, given back; scale buffers in TMEM: their MMAs are done
+  __shared__ __align__(8) uint64_t sfull_bar[kSlots], sblock_bar[kSlots], sempty_bar[kSlots], wdone_bar[C::kSfBufs];
   __shared__ __align__(8) uint64_t accf_bar[2], acce_bar[2], drain_bar;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh;
@@ -131,12 +129,10 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
     }
     for (int s = 0; s < kSlots; ++s) {
       ptx::mbar_init(ptx::smem_addr(&sfull_bar[s]), 1);
-      ptx::mbar_init(ptx::smem_addr(&sempty_bar[s]), kScaleWarps);
+      ptx::mbar_init(ptx::smem_addr(&sblock_bar[s]), kScaleWarps);
+      ptx::mbar_init(ptx::smem_addr(&sempty_bar[s]), 1);
     }
-    for (int b = 0; b < C::kSfBufs; ++b) {
-      ptx::mbar_init(ptx::smem_addr(&wfull_bar[b]), kScaleWarps / 2);
-      ptx::mbar_init(ptx::smem_addr(&wempty_bar[b]), 1);
-    }
+    for (int b = 0; b < C::kSfBufs; ++b) ptx::mbar_init(ptx::smem_addr(&wdone_bar[b]), 1);
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(ptx::smem_addr(&accf_bar[b]), 1);
       ptx::mbar_init(ptx::smem_addr(&acce_bar[b]), kEpiWarps);
@@ -194,7 +190,7 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
   const int MT = (a.N + kBM - 1) / kBM;
   const int KB = (a.K + 2 * kBKBytes - 1) / (2 * kBKBytes);
   const int stride = scale_stride(kNv, a.K);
-  const int chunks = stride / 16;  // 16 scale bytes per row: one TMEM buffer
+  const int chunks = stride / 16;  // 16 scale bytes of each row: one TMEM buffer, half a slot
   const int ntiles = ok ? first_sh[a.E] * MT : 0;
   const int mine = int(blockIdx.x) < ntiles ? (ntiles - 1 - int(blockIdx.x)) / int(gridDim.x) + 1 : 0;
 
@@ -232,10 +228,11 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
   auto stage = [&](int s) { return ptx::smem_addr(smem) + uint32_t(s) * C::kStageBytes; };
 
   // State that a role carries from one list of tiles to the next: its place in
-  // its ring and that place's phase, the same of the TMEM scale buffers, tiles
-  // done, copies it may have in flight.
-  int s = 0, wb = 0, it = 0, issued = 0;
-  uint32_t ph = 0, wph = 0;
+  // its ring and that place's phase, the same of the scale slots and the TMEM
+  // scale buffers, tiles done, copies it may have in flight (all rings full: no
+  // more than their depth).
+  int s = 0, ss = 0, wb = 0, it = 0, issued = 0;
+  uint32_t ph = 0, sph = 0, wph = 0;
 
   for (int first_tile = 0; first_tile < mine; first_tile += kListed) {
     const int n = min(kListed, mine - first_tile);
@@ -244,22 +241,12 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
     __syncthreads();
     if (warp == 0 && ptx::elect_one()) {
       // ------------------------------------------------ codes
-      int pi = 0, pkb = 0;  // the weights are brought to L2 up to this tile and stage
-      int ahead = 0;
       for (int i = 0; i < n; ++i) {
         const Tile ti = list_sh[i];
         const int boxes = (ti.rows + kBoxRows - 1) / kBoxRows;
         const uint32_t bytes = uint32_t(C::kABytes + boxes * kBoxRows * kBKBytes);
         int kb = 0;
         for (; kb < KB; ++kb) {
-          for (; ahead < kStages + kPrefetch && pi < n; ++ahead) {
-            if (i > 0 || ahead >= kStages) ptx::tma_prefetch_3d(&maps.wcodes, pkb * kBKBytes, list_sh[pi].m0, list_sh[pi].e);
-            if (++pkb == KB) {
-              pkb = 0;
-              ++pi;
-            }
-          }
-          --ahead;
           if (!ptx::mbar_wait(ptx::smem_addr(&empty_bar[s]), ph ^ 1u, abort_p)) break;
           const uint32_t bar = ptx::smem_addr(&full_bar[s]), dst = stage(s);
           ptx::mbar_arrive_expect_tx(bar, bytes);
@@ -282,43 +269,65 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
       // ------------------------------------------------ MMA issuer
       const uint32_t sf_base = tmem + 2 * kTN;
       const uint64_t da0 = ptx::smem_desc_k128(stage(0));
+      const uint64_t ds0 = ptx::smem_desc_rows16(ptx::smem_addr(smem) + C::kScaleAt);
       for (int i = 0; i < n; ++i, ++it) {
         const int N = (list_sh[i].rows + 15) & ~15;
         const uint32_t d = tmem + uint32_t((it & 1) * kTN);
         const uint32_t idesc = ptx::idesc_fp4<kNv>(kBM, N, 0), idesc2 = ptx::idesc_fp4<kNv>(kBM, N, kNv ? 0 : 2);
-        const uint32_t bcols = N > 128 ? 8 : 4;
         bool good = ptx::mbar_wait(ptx::smem_addr(&acce_bar[it & 1]), (uint32_t(it >> 1) & 1u) ^ 1u, abort_p);
         for (int kb = 0; kb < KB && good; ++kb) {
-          const bool second = !kNv && (kb & 1);  // MX: two stages share the scale words of a buffer
-          if (!second) good = ptx::mbar_wait(ptx::smem_addr(&wfull_bar[wb]), wph, abort_p);
+          const int ci = kNv ? kb : kb >> 1;             // MX: two stages share 16 scale bytes
+          const bool second = !kNv && (kb & 1);
+          const bool done = kNv || second || kb + 1 == KB;  // the chunk's last stage
+          if (!second) {
+            // the slot's blocks are ready; the MMAs that read this TMEM buffer last are done
+            if (!(ci & 1)) good = ptx::mbar_wait(ptx::smem_addr(&sblock_bar[ss]), sph, abort_p);
+            good = good && ptx::mbar_wait(ptx::smem_addr(&wdone_bar[wb]), wph ^ 1u, abort_p);
+          }
           if (!(good && ptx::mbar_wait(ptx::smem_addr(&full_bar[s]), ph, abort_p))) {
             good = false;
             break;
           }
           ptx::tc_fence_after();
+          const uint32_t sfa = sf_base + uint32_t(wb * C::kSfCols), sfb = sfa + 16;
           // descriptors count in 16 bytes
+          if (!second) {
+            const uint64_t ds = ds0 + uint32_t(ss * (C::kSlotBytes / 16) + (ci & 1) * 128);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              ptx::tmem_cp_32x128(sfa + 4 * w, ds + 32 * w);
+              ptx::tmem_cp_32x128(sfb + C::kBCols * w, ds + 256 + 32 * w);
+              if (C::kHalves == 2 && N > 128) ptx::tmem_cp_32x128(sfb + C::kBCols * w + 4, ds + 512 + 32 * w);
+            }
+          }
           const uint64_t da = da0 + uint32_t(s * (C::kStageBytes / 16)), db = da + C::kABytes / 16;
-          const uint32_t sfa = sf_base + uint32_t(wb * C::kSfCols) + (second ? 8 : 0);
-          const uint32_t sfb = sf_base + uint32_t(wb * C::kSfCols) + 16 + (second ? 2 * bcols : 0);
+          const uint32_t w0 = second ? 2 : 0;
           const int steps = (a.K - kb * 2 * kBKBytes + 63) / 64;  // K steps that are left
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks) {
-            constexpr int kPerWord = kNv ? 1 : 2;
+            const uint32_t w = w0 + (kNv ? ks : ks >> 1);
             if (ks < steps)
-              ptx::mma_fp4<kNv>(d, da + 2 * ks, db + 2 * ks, ks & 1 ? idesc2 : idesc, sfa + 4 * (ks / kPerWord),
-                                sfb + bcols * (ks / kPerWord), (kb | ks) != 0);
+              ptx::mma_fp4<kNv>(d, da + 2 * ks, db + 2 * ks, ks & 1 ? idesc2 : idesc, sfa + 4 * w, sfb + C::kBCols * w,
+                                (kb | ks) != 0);
           }
           ptx::mma_commit(ptx::smem_addr(&empty_bar[s]));
-          if (kNv || second || kb + 1 == KB) {
-            ptx::mma_commit(ptx::smem_addr(&wempty_bar[wb]));
+          if (++s == kStages) {
+            s = 0;
+            ph ^= 1u;
+          }
+          if (done) {
+            ptx::mma_commit(ptx::smem_addr(&wdone_bar[wb]));
             if (++wb == C::kSfBufs) {
               wb = 0;
               wph ^= 1u;
             }
-          }
-          if (++s == kStages) {
-            s = 0;
-            ph ^= 1u;
+            if ((ci & 1) || kb + 1 == KB) {
+              ptx::mma_commit(ptx::smem_addr(&sempty_bar[ss]));
+              if (++ss == kSlots) {
+                ss = 0;
+                sph ^= 1u;
+              }
+            }
           }
         }
         if (!good) {
@@ -335,17 +344,17 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
         const uint32_t bytes = uint32_t((kBM + boxes * kBoxRows) * kSlotRow);
         int x = 0;
         for (; x < stride; x += kSlotRow) {
-          if (!ptx::mbar_wait(ptx::smem_addr(&sempty_bar[s]), ph ^ 1u, abort_p)) break;
-          const uint32_t bar = ptx::smem_addr(&sfull_bar[s]);
-          const uint32_t dst = ptx::smem_addr(smem) + C::kScaleAt + s * C::kSlotBytes;
+          if (!ptx::mbar_wait(ptx::smem_addr(&sempty_bar[ss]), sph ^ 1u, abort_p)) break;
+          const uint32_t bar = ptx::smem_addr(&sfull_bar[ss]);
+          const uint32_t dst = ptx::smem_addr(smem) + C::kScaleAt + ss * C::kSlotBytes;
           ptx::mbar_arrive_expect_tx(bar, bytes);
           ptx::tma_load_3d(dst, &maps.wscales, x, ti.m0, ti.e, bar);
           for (int b = 0; b < boxes; ++b)
             ptx::tma_load_2d(dst + (kBM + b * kBoxRows) * kSlotRow, &maps.tscales, x, ti.row0 + b * kBoxRows, bar);
           issued = min(issued + 1, kSlots);
-          if (++s == kSlots) {
-            s = 0;
-            ph ^= 1u;
+          if (++ss == kSlots) {
+            ss = 0;
+            sph ^= 1u;
           }
         }
         if (x < stride) {
@@ -353,100 +362,81 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
           break;
         }
       }
-    } else if (warp >= 4 && warp < 12) {
-      // ------------------------------------------------ scales to TMEM
+    } else if (warp >= 4 && warp < 4 + kScaleWarps) {
+      // ------------------------------------------------ scales into blocks
       const int blocks = a.K / (kNv ? 16 : 32);
-      const uint32_t quarter = tmem + (uint32_t(32 * (warp & 3)) << 16) + 2 * kTN;
-      const int group = (warp >> 2) - 1;  // takes every other buffer
+      const int unit = warp - 4;  // weights, first 128 tokens, second 128 tokens
       bool good = true;
       for (int i = 0; i < n && good; ++i) {
-        const int rows = list_sh[i].rows;
-        const int nb = (rows + 31) / 32;
-        for (int ci = 0; ci < chunks; ++ci) {
-          const bool slot_done = (ci & 1) || ci + 1 == chunks;
-          if ((wb & 1) == group) {
-            good = warp_wait(sfull_bar[s], ph) && warp_wait(wempty_bar[wb], wph ^ 1u);
-            if (!good) {
-              fail(7000004);
-              break;
-            }
-            // 16 scale bytes of row 32 c + lane (32-byte swizzle: the halves
-            // of rows 4-7 of every 8 change places)
-            const uint8_t* raw = smem + C::kScaleAt + s * C::kSlotBytes + lane * kSlotRow +
-                                 (((ci & 1) ^ ((lane >> 2) & 1)) << 4);
-            uint4 v[4 + C::kBBlocks];
-#pragma unroll
-            for (int c = 0; c < 4 + C::kBBlocks; ++c)
-              if (c < 4 + nb) v[c] = *reinterpret_cast<const uint4*>(raw + 32 * c * kSlotRow);
-            const int left = blocks - 16 * ci;
-            if (left < 16) {  // what lies behind K counts as 0
-              uint32_t m[4];
-#pragma unroll
-              for (int w = 0; w < 4; ++w)
-                m[w] = left >= 4 * w + 4 ? 0xffffffffu : left <= 4 * w ? 0u : (1u << (8 * (left - 4 * w))) - 1;
-#pragma unroll
-              for (int c = 0; c < 4 + C::kBBlocks; ++c) {
-                v[c].x &= m[0];
-                v[c].y &= m[1];
-                v[c].z &= m[2];
-                v[c].w &= m[3];
-              }
-            }
-            ptx::tc_fence_after();
-            const uint32_t at = quarter + uint32_t(wb * C::kSfCols);
-            auto store16 = [&](uint32_t to, int c0) {  // 4 words of 4 blocks
-              uint32_t r[16];
-#pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                const uint4 q = c0 + c < 4 + C::kBBlocks ? v[c0 + c] : make_uint4(0, 0, 0, 0);
-                r[c] = q.x;
-                r[4 + c] = q.y;
-                r[8 + c] = q.z;
-                r[12 + c] = q.w;
-              }
-              ptx::tmem_st16(to, r);
-            };
-            store16(at, 0);
-            if (C::kBBlocks <= 4 || rows <= 128) {
-              store16(at + 16, 4);
-            } else {
-              uint32_t r[32];
-#pragma unroll
-              for (int c = 0; c < 8; ++c) {
-                const uint4 q = c < C::kBBlocks ? v[4 + c] : make_uint4(0, 0, 0, 0);
-                r[c] = q.x;
-                r[8 + c] = q.y;
-                r[16 + c] = q.z;
-                r[24 + c] = q.w;
-              }
-              ptx::tmem_st32(at + 16, r);
-            }
-            ptx::tmem_st_wait();
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&wfull_bar[wb]));
+        const int rows = unit == 0 ? kBM : list_sh[i].rows - 128 * (unit - 1);
+        for (int c0 = 0; c0 < chunks; c0 += 2) {
+          good = warp_wait(sfull_bar[ss], sph);
+          if (!good) {
+            fail(7000004);
+            break;
           }
-          if (slot_done) {  // both groups give every slot back
-            if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&sempty_bar[s]));
-            if (++s == kSlots) {
-              s = 0;
-              ph ^= 1u;
+          uint8_t* raw = smem + C::kScaleAt + ss * C::kSlotBytes + unit * 128 * kSlotRow;
+          if (unit <= C::kHalves && rows > 0) {
+            // rows 32 b + lane, both halves (32-byte swizzle: the halves of
+            // rows 4-7 of every 8 change places)
+            uint4 v[2][4];
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+              if (32 * b < rows) {
+                const uint8_t* r = raw + (32 * b + lane) * kSlotRow;
+                const int swap = (lane & 4) << 2;
+                v[0][b] = *reinterpret_cast<const uint4*>(r + swap);
+                v[1][b] = *reinterpret_cast<const uint4*>(r + (swap ^ 16));
+              } else {
+                v[0][b] = v[1][b] = make_uint4(0, 0, 0, 0);
+              }
             }
+            const int left = blocks - 16 * c0;  // scale bytes from here to the end of K
+            if (left < 32) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                uint32_t m[4];
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                  const int l = left - 16 * h - 4 * w;
+                  m[w] = l >= 4 ? 0xffffffffu : l <= 0 ? 0u : (1u << (8 * l)) - 1;
+                }
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                  v[h][b].x &= m[0];
+                  v[h][b].y &= m[1];
+                  v[h][b].z &= m[2];
+                  v[h][b].w &= m[3];
+                }
+              }
+            }
+            __syncwarp();  // all read before any writes
+            uint4* o = reinterpret_cast<uint4*>(raw) + lane;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              o[128 * h] = make_uint4(v[h][0].x, v[h][1].x, v[h][2].x, v[h][3].x);
+              o[128 * h + 32] = make_uint4(v[h][0].y, v[h][1].y, v[h][2].y, v[h][3].y);
+              o[128 * h + 64] = make_uint4(v[h][0].z, v[h][1].z, v[h][2].z, v[h][3].z);
+              o[128 * h + 96] = make_uint4(v[h][0].w, v[h][1].w, v[h][2].w, v[h][3].w);
+            }
+            ptx::fence_proxy_async_smem();  // written by threads, read by the tensor core's copies
           }
-          if (++wb == C::kSfBufs) {
-            wb = 0;
-            wph ^= 1u;
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&sblock_bar[ss]));
+          if (++ss == kSlots) {
+            ss = 0;
+            sph ^= 1u;
           }
         }
       }
-    } else if (warp >= 12) {
+    } else if (warp >= 8) {
       // ------------------------------------------------ epilogue
       constexpr int kTok = sizeof(OT) == 2 && kTN > 32 ? 32 : 16;  // tokens staged at a time
       constexpr int kPieces = 2 * sizeof(OT);                      // 16-byte pieces of a token's 32 values
       constexpr int kPerPiece = 16 / sizeof(OT);
       const int q = warp & 3;             // TMEM lane quarter this warp may read
-      const int half = (warp - 12) >> 2;  // two warps per quarter take turns
-      uint8_t* scratch = smem + C::kScratchAt + (warp - 12) * kScratch;
+      const int half = (warp - 8) >> 2;   // two warps per quarter take turns
+      uint8_t* scratch = smem + C::kScratchAt + (warp - 8) * kScratch;
       OT* out = static_cast<OT*>(a.out);
       const float ga = a.a_tscale ? *a.a_tscale : 1.f;
       for (int i = 0; i < n; ++i, ++it) {
@@ -497,6 +487,8 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
       const int from = ptx::elected_lane();
       s = __shfl_sync(0xffffffffu, s, from);
       ph = __shfl_sync(0xffffffffu, ph, from);
+      ss = __shfl_sync(0xffffffffu, ss, from);
+      sph = __shfl_sync(0xffffffffu, sph, from);
       wb = __shfl_sync(0xffffffffu, wb, from);
       wph = __shfl_sync(0xffffffffu, wph, from);
       it = __shfl_sync(0xffffffffu, it, from);
@@ -510,14 +502,21 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
   if (warp == 1 && ptx::elect_one()) {
     ptx::mma_commit(ptx::smem_addr(&drain_bar));
     ptx::mbar_wait(ptx::smem_addr(&drain_bar), 0, nullptr);
-  } else if (warp == 0 || warp == 2) {
-    const int depth = warp == 0 ? kStages : kSlots;
+  } else if (warp == 0) {
     for (int i = 0; i < issued; ++i) {
       if (--s < 0) {
-        s = depth - 1;
+        s = kStages - 1;
         ph ^= 1u;
       }
-      ptx::mbar_wait(ptx::smem_addr(warp == 0 ? &full_bar[s] : &sfull_bar[s]), ph, nullptr);
+      ptx::mbar_wait(ptx::smem_addr(&full_bar[s]), ph, nullptr);
+    }
+  } else if (warp == 2) {
+    for (int i = 0; i < issued; ++i) {
+      if (--ss < 0) {
+        ss = kSlots - 1;
+        sph ^= 1u;
+      }
+      ptx::mbar_wait(ptx::smem_addr(&sfull_bar[ss]), sph, nullptr);
     }
   }
   __syncthreads();
