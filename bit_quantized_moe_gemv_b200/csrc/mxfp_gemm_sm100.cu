@@ -63,7 +63,9 @@ struct Cfg {
   // 16 bytes of each row: 4 x 4 columns of weights, 4 x kBCols of tokens
   static constexpr int kBCols = 4 * kHalves;
   static constexpr int kSfCols = 4 * (4 + kBCols);
-  static constexpr int kSfBufs = (512 - 2 * kTN) / kSfCols >= 4 ? 4 : 2;
+  // as many as code stages: a stage that is full again tells that the MMAs of
+  // its last use are done, and with them those on the scale buffer's last use
+  static constexpr int kSfBufs = kStages;
   static constexpr int kCols = 2 * kTN + kSfBufs * kSfCols;
   static constexpr int kTmemCols = kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
   static_assert(kCols <= 512, "TMEM");
@@ -100,9 +102,8 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
   using C = Cfg<kTN, kStages>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ __align__(8) uint64_t full_bar[kStages], empty_bar[kStages];      // codes
-  // scales in shared memory: arrived, in blocks, given back; scale buffers in TMEM: their MMAs are done
-  __shared__ __align__(8) uint64_t sfull_bar[kSlots], sblock_bar[kSlots], sempty_bar[kSlots], wdone_bar[C::kSfBufs];
+  __shared__ __align__(8) uint64_t full_bar[kStages], empty_bar[kStages];                      // codes
+  __shared__ __align__(8) uint64_t sfull_bar[kSlots], sblock_bar[kSlots], sempty_bar[kSlots];  // scales: come, in blocks
   __shared__ __align__(8) uint64_t accf_bar[2], acce_bar[2], drain_bar;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh;
@@ -132,7 +133,6 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
       ptx::mbar_init(ptx::smem_addr(&sblock_bar[s]), kScaleWarps);
       ptx::mbar_init(ptx::smem_addr(&sempty_bar[s]), 1);
     }
-    for (int b = 0; b < C::kSfBufs; ++b) ptx::mbar_init(ptx::smem_addr(&wdone_bar[b]), 1);
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(ptx::smem_addr(&accf_bar[b]), 1);
       ptx::mbar_init(ptx::smem_addr(&acce_bar[b]), kEpiWarps);
@@ -232,7 +232,7 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
   // scale buffers, tiles done, copies it may have in flight (all rings full: no
   // more than their depth).
   int s = 0, ss = 0, wb = 0, it = 0, issued = 0;
-  uint32_t ph = 0, sph = 0, wph = 0;
+  uint32_t ph = 0, sph = 0;
 
   for (int first_tile = 0; first_tile < mine; first_tile += kListed) {
     const int n = min(kListed, mine - first_tile);
@@ -267,68 +267,100 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
       }
     } else if (warp == 1 && ptx::elect_one()) {
       // ------------------------------------------------ MMA issuer
-      const uint32_t sf_base = tmem + 2 * kTN;
+      // One thread feeds the tensor core, and a stage's MMAs take 4 x N / 2
+      // cycles: every instruction here counts. Descriptors and TMEM columns
+      // are carried along, and the next stage's barrier is looked at while
+      // this stage's MMAs are issued.
+      const uint32_t sf0 = tmem + 2 * kTN;
       const uint64_t da0 = ptx::smem_desc_k128(stage(0));
       const uint64_t ds0 = ptx::smem_desc_rows16(ptx::smem_addr(smem) + C::kScaleAt);
+      const uint32_t full0 = ptx::smem_addr(&full_bar[0]), empty0 = ptx::smem_addr(&empty_bar[0]);
+      const int full_stages = a.K / (2 * kBKBytes), tail_steps = (a.K - full_stages * 2 * kBKBytes + 63) / 64;
+      uint64_t da = da0 + uint32_t(s * (C::kStageBytes / 16)), ds = ds0 + uint32_t(ss * (C::kSlotBytes / 16));
+      uint32_t sf = sf0 + uint32_t(wb * C::kSfCols);
+      bool ready = false, sready = false;
       for (int i = 0; i < n; ++i, ++it) {
         const int N = (list_sh[i].rows + 15) & ~15;
+        const bool wide = N > 128;
         const uint32_t d = tmem + uint32_t((it & 1) * kTN);
         const uint32_t idesc = ptx::idesc_fp4<kNv>(kBM, N, 0), idesc2 = ptx::idesc_fp4<kNv>(kBM, N, kNv ? 0 : 2);
-        bool good = ptx::mbar_wait(ptx::smem_addr(&acce_bar[it & 1]), (uint32_t(it >> 1) & 1u) ^ 1u, abort_p);
-        for (int kb = 0; kb < KB && good; ++kb) {
-          const int ci = kNv ? kb : kb >> 1;             // MX: two stages share 16 scale bytes
-          const bool second = !kNv && (kb & 1);
-          const bool done = kNv || second || kb + 1 == KB;  // the chunk's last stage
-          if (!second) {
-            // the slot's blocks are ready; the MMAs that read this TMEM buffer last are done
-            if (!(ci & 1)) good = ptx::mbar_wait(ptx::smem_addr(&sblock_bar[ss]), sph, abort_p);
-            good = good && ptx::mbar_wait(ptx::smem_addr(&wdone_bar[wb]), wph ^ 1u, abort_p);
-          }
-          if (!(good && ptx::mbar_wait(ptx::smem_addr(&full_bar[s]), ph, abort_p))) {
-            good = false;
-            break;
-          }
+        uint32_t acc = 0;
+        // One stage: descriptors count in 16 bytes. `second`: MX, the other
+        // half of the scale words that the stage before copied.
+        auto step = [&](bool second, uint64_t dsc, int steps) {
+          if (!ready && !ptx::mbar_wait(full0 + 8 * s, ph, abort_p)) return false;
           ptx::tc_fence_after();
-          const uint32_t sfa = sf_base + uint32_t(wb * C::kSfCols), sfb = sfa + 16;
-          // descriptors count in 16 bytes
           if (!second) {
-            const uint64_t ds = ds0 + uint32_t(ss * (C::kSlotBytes / 16) + (ci & 1) * 128);
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-              ptx::tmem_cp_32x128(sfa + 4 * w, ds + 32 * w);
-              ptx::tmem_cp_32x128(sfb + C::kBCols * w, ds + 256 + 32 * w);
-              if (C::kHalves == 2 && N > 128) ptx::tmem_cp_32x128(sfb + C::kBCols * w + 4, ds + 512 + 32 * w);
+              ptx::tmem_cp_32x128(sf + 4 * w, dsc + 32 * w);
+              ptx::tmem_cp_32x128(sf + 16 + C::kBCols * w, dsc + 256 + 32 * w);
+              if (C::kHalves == 2 && wide) ptx::tmem_cp_32x128(sf + 16 + C::kBCols * w + 4, dsc + 512 + 32 * w);
             }
           }
-          const uint64_t da = da0 + uint32_t(s * (C::kStageBytes / 16)), db = da + C::kABytes / 16;
-          const uint32_t w0 = second ? 2 : 0;
-          const int steps = (a.K - kb * 2 * kBKBytes + 63) / 64;  // K steps that are left
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks) {
-            const uint32_t w = w0 + (kNv ? ks : ks >> 1);
+            const uint32_t w = (second ? 2 : 0) + (kNv ? ks : ks >> 1);
             if (ks < steps)
-              ptx::mma_fp4<kNv>(d, da + 2 * ks, db + 2 * ks, ks & 1 ? idesc2 : idesc, sfa + 4 * w, sfb + C::kBCols * w,
-                                (kb | ks) != 0);
+              ptx::mma_fp4<kNv>(d, da + 2 * ks, da + C::kABytes / 16 + 2 * ks, ks & 1 ? idesc2 : idesc, sf + 4 * w,
+                                sf + 16 + C::kBCols * w, acc);
+            acc = 1;
           }
-          ptx::mma_commit(ptx::smem_addr(&empty_bar[s]));
+          ptx::mma_commit(empty0 + 8 * s);
+          da += C::kStageBytes / 16;
           if (++s == kStages) {
             s = 0;
             ph ^= 1u;
+            da = da0;
           }
-          if (done) {
-            ptx::mma_commit(ptx::smem_addr(&wdone_bar[wb]));
-            if (++wb == C::kSfBufs) {
-              wb = 0;
-              wph ^= 1u;
-            }
-            if ((ci & 1) || kb + 1 == KB) {
-              ptx::mma_commit(ptx::smem_addr(&sempty_bar[ss]));
-              if (++ss == kSlots) {
-                ss = 0;
-                sph ^= 1u;
-              }
-            }
+          ready = ptx::mbar_test_wait(full0 + 8 * s, ph);
+          return true;
+        };
+        auto next_buffer = [&]() {  // of the scale words in TMEM
+          sf += C::kSfCols;
+          if (++wb == C::kSfBufs) {
+            wb = 0;
+            sf = sf0;
           }
+        };
+        auto next_slot = [&]() {
+          ptx::mma_commit(ptx::smem_addr(&sempty_bar[ss]));
+          ds += C::kSlotBytes / 16;
+          if (++ss == kSlots) {
+            ss = 0;
+            sph ^= 1u;
+            ds = ds0;
+          }
+          sready = ptx::mbar_test_wait(ptx::smem_addr(&sblock_bar[ss]), sph);
+        };
+        auto slot_ready = [&]() { return sready || ptx::mbar_wait(ptx::smem_addr(&sblock_bar[ss]), sph, abort_p); };
+        bool good = ptx::mbar_wait(ptx::smem_addr(&acce_bar[it & 1]), (uint32_t(it >> 1) & 1u) ^ 1u, abort_p);
+        constexpr int kPerSlot = kNv ? 2 : 4;  // stages whose scales a slot holds
+        int kb = 0;
+        for (; kb + kPerSlot <= full_stages && good; kb += kPerSlot) {
+          good = slot_ready();
+          if (kNv) {
+            good = good && step(false, ds, 4);
+            next_buffer();
+            good = good && step(false, ds + 128, 4);
+          } else {
+            good = good && step(false, ds, 4) && step(true, ds, 4);
+            next_buffer();
+            good = good && step(false, ds + 128, 4) && step(true, ds + 128, 4);
+          }
+          next_buffer();
+          next_slot();
+        }
+        if (kb < KB && good) {  // the slot that K ends in
+          const int kb0 = kb;
+          good = slot_ready();
+          for (; kb < KB && good; ++kb) {
+            const int j = kb - kb0;
+            const bool second = !kNv && (j & 1);
+            good = step(second, ds + ((kNv ? j : j >> 1) & 1) * 128, kb < full_stages ? 4 : tail_steps);
+            if (kNv || second || kb + 1 == KB) next_buffer();
+          }
+          next_slot();
         }
         if (!good) {
           fail(7000002);
@@ -490,7 +522,6 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
       ss = __shfl_sync(0xffffffffu, ss, from);
       sph = __shfl_sync(0xffffffffu, sph, from);
       wb = __shfl_sync(0xffffffffu, wb, from);
-      wph = __shfl_sync(0xffffffffu, wph, from);
       it = __shfl_sync(0xffffffffu, it, from);
       issued = __shfl_sync(0xffffffffu, issued, from);
     }
@@ -585,7 +616,7 @@ cudaError_t run_tiles(const Maps& m, const Args& a, cudaStream_t st) {
   // few rows per expert: narrow tiles leave room for a ring twice as deep, and
   // the weights stream through it
   if (a.R <= 32LL * a.E) return run<kNv, 32, 8, OT>(m, a, st);
-  return run<kNv, 192, 4, OT>(m, a, st);
+  return run<kNv, 160, 4, OT>(m, a, st);
 }
 
 template <bool kNv>
