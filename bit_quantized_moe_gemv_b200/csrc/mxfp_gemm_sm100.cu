@@ -25,9 +25,12 @@
 // tcgen05.cp SPEED_CP us (the MMAs alone take 141).
 //
 // Tiles: every CTA sums up the experts' token tiles (offsets are on the
-// device) and takes tiles b, b + grid, ... of the list "expert, token tile, 128
-// weight rows": neighbours share the tokens, and an expert's weights are read
-// from HBM once, later token tiles hit L2. What a tile is (expert, rows) is
+// device) and takes tiles b, b + grid, ... of the list "token tile, 128 weight
+// rows": neighbours share the tokens. Token tiles of experts with several of
+// them, bound by L2 and the tensor core, alternate with those of experts with
+// one, bound by HBM (8K tokens with Zipf routing, SPEED_ORDER us in the
+// experts' order); each kind keeps the experts' order, so that an expert's
+// weights are read from HBM once and its later token tiles hit L2. What a tile is (expert, rows) is
 // worked out by all threads at once for the next kListed tiles of the CTA: the
 // search and the divisions cost a single warp about 900 cycles a tile.
 #include <cuda.h>
@@ -48,13 +51,13 @@ constexpr int kBoxRows = 32;   // token rows per TMA box
 constexpr int kThreads = 512;
 constexpr int kEpiWarps = 8, kScaleWarps = 3;
 constexpr int kSlotRow = 32;   // scale bytes of a row per slot
-constexpr int kSlots = 3;
-constexpr int kListed = 256;  // tiles listed at a time
 constexpr int kScratch = 2048;  // epilogue staging per warp: 32 weight rows of 32 (16 bits) or 16 tokens
 
-// kTN: tokens per tile (a multiple of 32); kStages: ring depth.
-template <int kTN, int kStages>
+// kTN: tokens per tile (a multiple of 32); kStages, kSlots: depth of the rings of codes and of scales.
+template <int kTN, int kStages, int kSlots>
 struct Cfg {
+  static constexpr bool kNarrow = kTN <= 32;  // two CTAs per SM
+  static constexpr int kListed = kNarrow ? 128 : 256;  // tiles listed at a time
   static constexpr int kHalves = (kTN + 127) / 128;  // 128-row scale blocks of the token side
   static constexpr int kABytes = kBM * kBKBytes;
   static constexpr int kStageBytes = kABytes + kTN * kBKBytes;
@@ -96,10 +99,10 @@ struct alignas(16) Tile {
 // Token tiles of an expert with `rows` rows.
 __device__ __forceinline__ int token_tiles(int rows, int tn) { return (rows + tn - 1) / tn; }
 
-template <bool kNv, int kTN, int kStages, typename OT>
-__global__ void __launch_bounds__(kThreads, 1)
+template <bool kNv, int kTN, int kStages, int kSlots, typename OT>
+__global__ void __launch_bounds__(kThreads, Cfg<kTN, kStages, kSlots>::kNarrow ? 2 : 1)
 fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
-  using C = Cfg<kTN, kStages>;
+  using C = Cfg<kTN, kStages, kSlots>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ __align__(8) uint64_t full_bar[kStages], empty_bar[kStages];                      // codes
@@ -107,10 +110,12 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
   __shared__ __align__(8) uint64_t accf_bar[2], acce_bar[2], drain_bar;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh;
-  __shared__ int off_sh[kMaxE + 1];    // first row of each expert
-  __shared__ int first_sh[kMaxE + 1];  // first token tile of each expert
-  __shared__ int wsum_sh[kThreads / 32];
-  __shared__ Tile list_sh[kListed];
+  constexpr int kExperts = C::kNarrow ? 1 : kMaxE + 1;
+  __shared__ int off_sh[kExperts];       // first row of each expert
+  __shared__ int first_sh[2][kExperts];  // its first token tile among experts with one, with several
+  __shared__ int wsum_sh[2][kThreads / 32];
+  __shared__ int all_sh;                 // token tiles
+  __shared__ Tile list_sh[C::kListed];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort_p = &abort_sh;
@@ -150,7 +155,7 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
     ptx::tma_prefetch_map(&maps.tscales);
   }
   bool ok = true;
-  int cnt[kPer], sum = 0;
+  int cnt[kPer], one = 0, many = 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int e = threadIdx.x * kPer + i;
@@ -161,26 +166,39 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
       else
         cnt[i] = token_tiles(row_at[i + 1] - row_at[i], kTN);
     }
-    sum += cnt[i];
+    (!C::kNarrow && cnt[i] > 1 ? many : one) += cnt[i];
   }
-  int incl = sum;
+  int incl1 = one, incl2 = many;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
+    const int u = __shfl_up_sync(0xffffffffu, incl1, o), v = __shfl_up_sync(0xffffffffu, incl2, o);
+    if (lane >= o) {
+      incl1 += u;
+      incl2 += v;
+    }
   }
-  if (lane == 31) wsum_sh[warp] = incl;
+  if (lane == 31) {
+    wsum_sh[0][warp] = incl1;
+    wsum_sh[1][warp] = incl2;
+  }
   ok = !__syncthreads_or(!ok);
-  int base = incl - sum;
-  for (int w = 0; w < warp; ++w) base += wsum_sh[w];
+  int base1 = incl1 - one, base2 = incl2 - many;
+  for (int w = 0; w < warp; ++w) {
+    base1 += wsum_sh[0][w];
+    base2 += wsum_sh[1][w];
+  }
+  int first_of[kPer];  // first token tiles of this thread's experts
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int e = threadIdx.x * kPer + i;
-    if (e <= a.E) {
+    first_of[i] = base1;
+    if (!C::kNarrow && e <= a.E) {
       off_sh[e] = row_at[i];
-      first_sh[e] = base;
+      first_sh[0][e] = base1;
+      first_sh[1][e] = base2;
     }
-    base += cnt[i];
+    if (C::kNarrow && e == a.E) all_sh = base1;
+    (!C::kNarrow && cnt[i] > 1 ? base2 : base1) += cnt[i];
   }
   if (!ok && threadIdx.x == 0) flag_error(a.hdr, MOE_ERR_DEVICE_FAULT, -1);
   ptx::tc_fence_before();
@@ -191,20 +209,47 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
   const int KB = (a.K + 2 * kBKBytes - 1) / (2 * kBKBytes);
   const int stride = scale_stride(kNv, a.K);
   const int chunks = stride / 16;  // 16 scale bytes of each row: one TMEM buffer, half a slot
-  const int ntiles = ok ? first_sh[a.E] * MT : 0;
+  // token tiles of experts with one (narrow tiles: of all), and with several
+  const int ones = C::kNarrow ? all_sh : first_sh[0][a.E], manys = C::kNarrow ? 0 : first_sh[1][a.E];
+  const int ntiles = ok ? (ones + manys) * MT : 0;
   const int mine = int(blockIdx.x) < ntiles ? (ntiles - 1 - int(blockIdx.x)) / int(gridDim.x) + 1 : 0;
 
+  // The CTA's tiles [from, from + n) into the list. Few rows: every expert's
+  // thread writes its own, which takes the fewest instructions. Else thread i
+  // finds the i-th.
+  auto write_list = [&](int from, int n) {
+    for (int i = 0; i < kPer; ++i) {
+      const int rows = row_at[i + 1] - row_at[i], t0 = first_of[i] * MT, t1 = (first_of[i] + cnt[i]) * MT;
+      if (cnt[i] == 0) continue;
+      // the CTA's first tile from t0 on, as its place in the list
+      int at = max(0, int(uint32_t(max(t0 - int(blockIdx.x), 0) + int(gridDim.x) - 1) / gridDim.x) - from);
+      for (; at < n; ++at) {
+        const int t = int(blockIdx.x) + (from + at) * int(gridDim.x);
+        if (t >= t1) break;
+        const int tt = int(uint32_t(t - t0) / uint32_t(MT)), row0 = tt * kTN;
+        list_sh[at] = Tile{int(threadIdx.x) * kPer + i, (t - t0 - tt * MT) * kBM, row_at[i] + row0, min(kTN, rows - row0)};
+      }
+    }
+  };
   auto tile_at = [&](int t) {
     const int tt = int(uint32_t(t) / uint32_t(MT));
-    int e = 0, hi = a.E;  // the last expert whose first token tile is <= tt
+    // of the first tt token tiles, tt * manys / all are of experts with several
+    int kind = 0, at = tt;
+    if (manys) {
+      const int before = int(uint64_t(tt) * uint32_t(manys) / uint32_t(ones + manys));
+      kind = int(uint64_t(tt + 1) * uint32_t(manys) / uint32_t(ones + manys)) > before;
+      at = kind ? before : tt - before;
+    }
+    const int* first = first_sh[kind];
+    int e = 0, hi = a.E;  // the last expert whose first token tile of this kind is <= at
     while (hi - e > 1) {
       const int mid = (e + hi) >> 1;
-      if (first_sh[mid] <= tt)
+      if (first[mid] <= at)
         e = mid;
       else
         hi = mid;
     }
-    const int lo = off_sh[e], rows = off_sh[e + 1] - lo, nt = first_sh[e + 1] - first_sh[e], i = tt - first_sh[e];
+    const int lo = off_sh[e], rows = off_sh[e + 1] - lo, nt = first[e + 1] - first[e], i = at - first[e];
     // token tiles of one size, a multiple of 16 (at most kTN, so none is empty)
     const int per = nt == 1 ? rows : (int(uint32_t(rows + nt - 1) / uint32_t(nt)) + 15) & ~15;
     return Tile{e, (t - tt * MT) * kBM, lo + i * per, min(per, rows - i * per)};
@@ -234,9 +279,11 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
   int s = 0, ss = 0, wb = 0, it = 0, issued = 0;
   uint32_t ph = 0, sph = 0;
 
-  for (int first_tile = 0; first_tile < mine; first_tile += kListed) {
-    const int n = min(kListed, mine - first_tile);
-    if (int(threadIdx.x) < n)
+  for (int first_tile = 0; first_tile < mine; first_tile += C::kListed) {
+    const int n = min(C::kListed, mine - first_tile);
+    if (C::kNarrow)
+      write_list(first_tile, n);
+    else if (int(threadIdx.x) < n)
       list_sh[threadIdx.x] = tile_at(int(blockIdx.x) + (first_tile + int(threadIdx.x)) * int(gridDim.x));
     __syncthreads();
     if (warp == 0 && ptx::elect_one()) {
@@ -597,15 +644,15 @@ int sm_count() {
   return n;
 }
 
-template <bool kNv, int kTN, int kStages, typename OT>
+template <bool kNv, int kTN, int kStages, int kSlots, typename OT>
 cudaError_t run(const Maps& m, const Args& a, cudaStream_t st) {
-  using C = Cfg<kTN, kStages>;
-  auto* kernel = fp4_gemm_kernel<kNv, kTN, kStages, OT>;
+  using C = Cfg<kTN, kStages, kSlots>;
+  auto* kernel = fp4_gemm_kernel<kNv, kTN, kStages, kSlots, OT>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   // at most this many tiles: every group with rows may end in a partial one
   const long long most = ((long long)a.R / kTN + (a.R < a.E ? a.R : a.E) + 1) * ((a.N + kBM - 1) / kBM);
-  const int sms = sm_count();
+  const int sms = sm_count() * (C::kNarrow ? 2 : 1);
   kernel<<<unsigned(most < sms ? most : sms), kThreads, C::kSmem, st>>>(m, a);
   count_launches(1);
   return cudaGetLastError();
@@ -615,8 +662,8 @@ template <bool kNv, typename OT>
 cudaError_t run_tiles(const Maps& m, const Args& a, cudaStream_t st) {
   // few rows per expert: narrow tiles leave room for a ring twice as deep, and
   // the weights stream through it
-  if (a.R <= 32LL * a.E) return run<kNv, 32, 8, OT>(m, a, st);
-  return run<kNv, 160, 4, OT>(m, a, st);
+  if (a.R <= 32LL * a.E) return run<kNv, 32, 3, 3, OT>(m, a, st);
+  return run<kNv, 160, 4, 3, OT>(m, a, st);
 }
 
 template <bool kNv>
