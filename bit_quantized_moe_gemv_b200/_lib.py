@@ -94,6 +94,8 @@ def _load():
 
 
 LIB = _load()
+_REAL = LIB     # the library the fast path is bound to (tests put others in LIB's place)
+_native = None  # the fast path, bound on first use: it needs torch's libraries
 
 
 def launch_count() -> int:
@@ -300,6 +302,20 @@ _codes = {}    # torch.dtype -> MOE_DT_*
 _raw_stream = None
 
 
+def _fast():
+    """The module of csrc/binding.cpp, which makes a call whose arguments are
+    plainly right without the checks below; there is no running without it."""
+    global _native
+    if _native is None:
+        _rt()
+        if not os.path.exists(_build.NATIVE):
+            raise ImportError(f"{_build.NATIVE} is missing: build it with `python -m bit_quantized_moe_gemv_b200.build`")
+        from . import _native as m
+        m.bind(LIB._name)
+        _native = m
+    return _native
+
+
 def _rt():
     """Set up on the first call: importing torch here keeps the module's import
     light, and a call's checks cost less than its launch."""
@@ -389,6 +405,12 @@ def _status_ws(ws, dev):
 
 def permute(x, inv_perm, x_perm, ws, stream=None):
     """moe_permute: x [T, H] to the rows x_perm [T*k, H] sorted by expert."""
+    if stream is None and LIB is _REAL:
+        st = (_native or _fast()).permute(x, inv_perm, x_perm, ws)
+        if st == 0:
+            return
+        if st > 0:
+            raise MoeError("moe_permute", st)
     dev = _device()
     T, H, d, code = _rows_of(x, "x", True)
     if T == 0:
@@ -402,6 +424,12 @@ def permute(x, inv_perm, x_perm, ws, stream=None):
 
 def permute_grad(dx_perm, inv_perm, dx, ws, stream=None):
     """moe_permute_grad: dx [T, H], the sum of each token's rows of dx_perm."""
+    if stream is None and LIB is _REAL:
+        st = (_native or _fast()).permute_grad(dx_perm, inv_perm, dx, ws)
+        if st == 0:
+            return
+        if st > 0:
+            raise MoeError("moe_permute_grad", st)
     dev = _device()
     T, H, d, code = _rows_of(dx, "dx")
     if T == 0:
@@ -415,6 +443,12 @@ def permute_grad(dx_perm, inv_perm, dx, ws, stream=None):
 
 def unpermute(y_perm, inv_perm, topk_w, out, ws, stream=None):
     """moe_unpermute: out [T, H], each token's rows weighted by topk_w [T, k]."""
+    if stream is None and LIB is _REAL:
+        st = (_native or _fast()).unpermute(y_perm, inv_perm, topk_w, out, ws)
+        if st == 0:
+            return
+        if st > 0:
+            raise MoeError("moe_unpermute", st)
     dev = _device()
     T, H, d, code = _rows_of(out, "out")
     if T == 0:
@@ -429,6 +463,12 @@ def unpermute(y_perm, inv_perm, topk_w, out, ws, stream=None):
 
 def unpermute_grad(dout, y_perm, inv_perm, topk_w, dy_perm, dtopk_w, ws, stream=None):
     """moe_unpermute_grad: the gradients of y_perm and topk_w from dout [T, H]."""
+    if stream is None and LIB is _REAL:
+        st = (_native or _fast()).unpermute_grad(dout, y_perm, inv_perm, topk_w, dy_perm, dtopk_w, ws)
+        if st == 0:
+            return
+        if st > 0:
+            raise MoeError("moe_unpermute_grad", st)
     dev = _device()
     T, H, d, code = _rows_of(dout, "dout")
     if T == 0:
@@ -465,6 +505,12 @@ def _stride(cols, fmt):  # moe_mxfp_scale_stride without a call
 def mxfp_quantize(x, codes, scales, fmt, tensor_scale=None, swiglu=False, rows_dev=None, stream=None):
     """moe_mxfp_quantize: x [rows, cols] (with swiglu: gate | up [rows, 2*cols])
     to codes [rows, cols/2] and scales [rows, mxfp_scale_stride(cols, fmt)]."""
+    if stream is None and LIB is _REAL:
+        st = (_native or _fast()).quantize(x, codes, scales, fmt, tensor_scale, swiglu, rows_dev)
+        if st == 0:
+            return
+        if st > 0:
+            raise MoeError("moe_mxfp_quantize", st)
     dev, f = _device(), _format(fmt)
     rows, wide, d, code = _rows_of(x, "x")
     cols = wide
@@ -483,6 +529,12 @@ def mxfp_quantize(x, codes, scales, fmt, tensor_scale=None, swiglu=False, rows_d
 
 def mxfp_dequantize(codes, scales, out, fmt, tensor_scale=None, rows_dev=None, stream=None):
     """moe_mxfp_dequantize: the values of codes and scales into out [rows, cols]."""
+    if stream is None and LIB is _REAL:
+        st = (_native or _fast()).dequantize(codes, scales, out, fmt, tensor_scale, rows_dev)
+        if st == 0:
+            return
+        if st > 0:
+            raise MoeError("moe_mxfp_dequantize", st)
     dev, f = _device(), _format(fmt)
     rows, cols, d, code = _rows_of(out, "out")
     u8 = _torch.uint8
@@ -499,6 +551,13 @@ def mxfp_matmul(a_codes, a_scales, b_codes, b_scales, out, fmt, ws, offsets=None
                 b_tensor_scale=None, stream=None):
     """moe_mxfp_matmul: rows a [R, K] times their expert's b [E, N, K] into out
     [R, N]; offsets [E+1] as moe_dispatch writes them (None: E = 1)."""
+    if stream is None and LIB is _REAL:
+        st = (_native or _fast()).matmul(a_codes, a_scales, b_codes, b_scales, out, fmt, ws, offsets, a_tensor_scale,
+                                     b_tensor_scale)
+        if st == 0:
+            return
+        if st > 0:
+            raise MoeError("moe_mxfp_matmul", st)
     dev, f = _device(), _format(fmt)
     R, N, d, code = _rows_of(out, "out")
     if b_codes is None or b_codes.dim() != 3:

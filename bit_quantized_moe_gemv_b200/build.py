@@ -1,4 +1,5 @@
-"""Build the in-tree CUDA library libmoe_b200.so for sm_100a with nvcc.
+"""Build the in-tree CUDA library libmoe_b200.so for sm_100a with nvcc, and the
+fast path of its Python binding (_native.so) with g++ against torch's headers.
 
     python -m bit_quantized_moe_gemv_b200.build [--force]
 """
@@ -16,6 +17,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmoe_b200.so")
+NATIVE = os.path.join(PKG, "_native.so")
 OBJ_DIR = os.path.join(ROOT, "_build")
 
 NVCC_FLAGS = [
@@ -41,15 +43,42 @@ def _deps():
         glob.glob(os.path.join(INCLUDE, "*.h"))
 
 
+def _newer(out, deps) -> bool:
+    return os.path.exists(out) and all(os.path.getmtime(p) <= os.path.getmtime(out) for p in deps)
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
-        return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    return _newer(LIB, _deps())
+
+
+def build_native(force: bool = False) -> str:
+    """The binding's fast path: a CPython module over torch's C++ tensors."""
+    src = os.path.join(CSRC, "binding.cpp")
+    if not force and _newer(NATIVE, [src, os.path.join(INCLUDE, "moe.h")]):
+        return NATIVE
+    import sysconfig
+
+    import torch
+    t = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    tmp = NATIVE + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           "-isystem", os.path.join(t, "include"),
+           "-isystem", os.path.join(t, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(cuda, "include"), "-isystem", sysconfig.get_paths()["include"], src, "-o", tmp,
+           "-L", os.path.join(t, "lib"), f"-Wl,-rpath,{os.path.join(t, 'lib')}", "-ltorch_python", "-ltorch_cpu",
+           "-lc10_cuda", "-lc10", "-ldl"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {src}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, NATIVE)
+    return NATIVE
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
+        build_native()
         return LIB
     nvcc = _nvcc()
     os.makedirs(OBJ_DIR, exist_ok=True)
@@ -65,7 +94,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
+        native = ex.submit(build_native, force)
         objs = list(ex.map(compile_one, sources()))
+        native.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc, "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -185,3 +185,29 @@ def test_the_reference_rounds_by_hand():
     v = ref.values(ref.pack(code), ref.pad_scales(byte, 32, "nv"), "nv", 0.5)
     assert v[0, :2].tolist() == [6.0, -2.0]
     assert ref.e4m3_table("cpu")[[1, 7, 8, 56, 126]].tolist() == [2.0 ** -9, 7 * 2.0 ** -9, 2.0 ** -6, 1.0, 448.0]
+
+
+def test_the_fast_path_leaves_everything_doubtful_to_the_checks(L):
+    """The native half of the binding answers -1, without a call, to anything
+    that is not plainly right: here to host tensors, other objects, wrong counts."""
+    f = L._fast()
+    inv, ws, w = _i32(12), _u8(8704), torch.zeros(4, 3)
+    good = {
+        "permute": [_bf(4, 64), inv, _bf(12, 64), ws],
+        "permute_grad": [_bf(12, 64), inv, _bf(4, 64), ws],
+        "unpermute": [_bf(12, 64), inv, w, _bf(4, 64), ws],
+        "unpermute_grad": [_bf(4, 64), _bf(12, 64), inv, w, _bf(12, 64), w.clone(), ws],
+        "quantize": [_bf(4, 64), _u8(4, 32), _u8(4, 16), "mx", None, False, None],
+        "dequantize": [_u8(4, 32), _u8(4, 16), _bf(4, 64), "mx", None, None],
+        "matmul": [_u8(4, 32), _u8(4, 16), _u8(3, 16, 32), _u8(3, 16, 16), _bf(4, 16), "mx", ws, _i32(4), None, None],
+    }
+    for name, args in good.items():
+        call = getattr(f, name)
+        assert call(*args) == -1  # tensors of the host
+        assert call(*args[:-1]) == -1 and call(*args, None) == -1 and call() == -1
+        for i in range(len(args)):
+            for other in (None, 3, "x", object()):
+                assert call(*args[:i], other, *args[i + 1:]) == -1
+    with pytest.raises(ImportError):
+        f.bind("/nowhere/libmoe_b200.so")
+    f.bind(L._build.LIB)
