@@ -120,14 +120,6 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort_p = &abort_sh;
 
-  // ---- the running sum of token tiles; barriers and TMEM meanwhile
-  constexpr int kPer = (kMaxE + kThreads - 1) / kThreads;
-  int row_at[kPer + 1];
-#pragma unroll
-  for (int i = 0; i <= kPer; ++i) {
-    const int e = threadIdx.x * kPer + i;
-    row_at[i] = e > a.E ? 0 : a.offsets ? a.offsets[e] : e ? a.R : 0;
-  }
   if (warp == 0 && lane == 0) {
     for (int s = 0; s < kStages; ++s) {
       ptx::mbar_init(ptx::smem_addr(&full_bar[s]), 1);
@@ -153,6 +145,15 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
     ptx::tma_prefetch_map(&maps.tcodes);
     ptx::tma_prefetch_map(&maps.wscales);
     ptx::tma_prefetch_map(&maps.tscales);
+  }
+  chain_wait();
+  // ---- the running sum of token tiles
+  constexpr int kPer = (kMaxE + kThreads - 1) / kThreads;
+  int row_at[kPer + 1];
+#pragma unroll
+  for (int i = 0; i <= kPer; ++i) {
+    const int e = threadIdx.x * kPer + i;
+    row_at[i] = e > a.E ? 0 : a.offsets ? a.offsets[e] : e ? a.R : 0;
   }
   bool ok = true;
   int cnt[kPer], one = 0, many = 0;
@@ -204,6 +205,7 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
+  chain_go();  // every CTA has its TMEM: a successor that waits for some takes none from this grid
   const uint32_t tmem = tmem_base_sh;
   const int MT = (a.N + kBM - 1) / kBM;
   const int KB = (a.K + 2 * kBKBytes - 1) / (2 * kBKBytes);
@@ -653,9 +655,7 @@ cudaError_t run(const Maps& m, const Args& a, cudaStream_t st) {
   // at most this many tiles: every group with rows may end in a partial one
   const long long most = ((long long)a.R / kTN + (a.R < a.E ? a.R : a.E) + 1) * ((a.N + kBM - 1) / kBM);
   const int sms = sm_count() * (C::kNarrow ? 2 : 1);
-  kernel<<<unsigned(most < sms ? most : sms), kThreads, C::kSmem, st>>>(m, a);
-  count_launches(1);
-  return cudaGetLastError();
+  return launch_chained(kernel, dim3(unsigned(most < sms ? most : sms)), kThreads, C::kSmem, st, m, a);
 }
 
 template <bool kNv, typename OT>

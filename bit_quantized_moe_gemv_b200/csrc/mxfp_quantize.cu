@@ -320,6 +320,8 @@ quantize_kernel(const T* __restrict__ x, long long rows, WarpSplit ws, int scale
                 const float* __restrict__ tscale, const int* __restrict__ rows_dev, uint32_t* __restrict__ codes,
                 uint8_t* __restrict__ scales) {
   constexpr int kLanes = kNv ? 2 : 4;
+  chain_go();
+  chain_wait();
   const float g = kNv && tscale ? *tscale : 1.f;
   const float inv6g = 1.f / (6.f * g);
   const uint32_t warp = blockIdx.x * (kThreads / 32) + threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -367,6 +369,8 @@ dequantize_kernel(const uint32_t* __restrict__ codes, const uint8_t* __restrict_
                   int scale_stride, const float* __restrict__ tscale, const int* __restrict__ rows_dev,
                   T* __restrict__ out) {
   constexpr int kLanes = kNv ? 2 : 4;
+  chain_go();
+  chain_wait();
   const float g = kNv && tscale ? *tscale : 1.f;
   const long long limit = rows_in_use(rows_dev, rows) * sp.per_row;
   const long long n0 = (long long)blockIdx.x * (kThreads * kUnroll) + threadIdx.x;
@@ -420,21 +424,15 @@ cudaError_t run_quantize(const void* x, long long rows, int cols, const float* t
   const T* in = static_cast<const T*>(x);
   uint32_t* out = static_cast<uint32_t*>(codes);
   const int stride = scale_stride(kNv, cols), per_row = cols / 8;
-  auto launch = [&](auto kernel, const WarpSplit& ws) {
+  auto launch = [&](auto* kernel, const WarpSplit& ws) {
     const unsigned grid = unsigned((ws.warps + kThreads / 32 - 1) / (kThreads / 32));
-    kernel<<<grid, kThreads, 0, st>>>(in, rows, ws, stride, tscale, rows_dev, out, scales);
+    return launch_chained(kernel, dim3(grid), kThreads, 0, st, in, rows, ws, stride, tscale, rows_dev, out, scales);
   };
-  if (rows * per_row < 148LL * 8 * kThreads * kUnroll) {
-    launch(quantize_kernel<T, kNv, kSwiglu, 1>, warp_split(rows, per_row, 1));
-  } else {
-    const WarpSplit a = warp_split(rows, per_row, kUnroll), b = warp_split(rows, per_row, 3);
-    if (a.parts * kUnroll <= b.parts * 3)
-      launch(quantize_kernel<T, kNv, kSwiglu, kUnroll>, a);
-    else
-      launch(quantize_kernel<T, kNv, kSwiglu, 3>, b);
-  }
-  count_launches(1);
-  return cudaGetLastError();
+  if (rows * per_row < 148LL * 8 * kThreads * kUnroll)
+    return launch(quantize_kernel<T, kNv, kSwiglu, 1>, warp_split(rows, per_row, 1));
+  const WarpSplit a = warp_split(rows, per_row, kUnroll), b = warp_split(rows, per_row, 3);
+  return a.parts * kUnroll <= b.parts * 3 ? launch(quantize_kernel<T, kNv, kSwiglu, kUnroll>, a)
+                                          : launch(quantize_kernel<T, kNv, kSwiglu, 3>, b);
 }
 
 template <typename T>
@@ -455,18 +453,10 @@ cudaError_t dequantize_as(bool nv, const void* codes, const uint8_t* scales, lon
   const bool big = sp.total >= 148LL * 8 * kThreads * 4;  // as above
   const int per = kThreads * (big ? 4 : 1);
   const unsigned grid = unsigned((sp.total + per - 1) / per);
-  const uint32_t* c = static_cast<const uint32_t*>(codes);
-  T* o = static_cast<T*>(out);
-  if (nv && big)
-    dequantize_kernel<T, true, 4><<<grid, kThreads, 0, st>>>(c, scales, rows, sp, stride, tscale, rows_dev, o);
-  else if (nv)
-    dequantize_kernel<T, true, 1><<<grid, kThreads, 0, st>>>(c, scales, rows, sp, stride, tscale, rows_dev, o);
-  else if (big)
-    dequantize_kernel<T, false, 4><<<grid, kThreads, 0, st>>>(c, scales, rows, sp, stride, tscale, rows_dev, o);
-  else
-    dequantize_kernel<T, false, 1><<<grid, kThreads, 0, st>>>(c, scales, rows, sp, stride, tscale, rows_dev, o);
-  count_launches(1);
-  return cudaGetLastError();
+  auto* kernel = nv ? big ? dequantize_kernel<T, true, 4> : dequantize_kernel<T, true, 1>
+                    : big ? dequantize_kernel<T, false, 4> : dequantize_kernel<T, false, 1>;
+  return launch_chained(kernel, dim3(grid), kThreads, 0, st, static_cast<const uint32_t*>(codes), scales, rows, sp,
+                        stride, tscale, rows_dev, static_cast<T*>(out));
 }
 
 // Shared by both directions. The chunk count is bounded by the grid: 2^31

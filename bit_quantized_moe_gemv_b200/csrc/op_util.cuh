@@ -35,9 +35,33 @@ inline int dtype_size(int32_t dtype) {
   }
 }
 
-__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
-__device__ __forceinline__ float to_f32(float v) { return v; }
+// Chained launches: the kernel may be started while its predecessor on the
+// stream still runs, and touches no memory before chain_wait, which returns
+// when the predecessor is done and its writes are seen. A predecessor of this
+// kind lets it start at chain_go, any other at its end. What runs before the
+// wait (barriers, TMEM, descriptors) and the launch itself then cost nothing: a
+// chain of small calls takes the host's 3 to 4 us each instead of 4.1 to 5.
+__device__ __forceinline__ void chain_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void chain_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename... Params, typename... Actual>
+cudaError_t launch_chained(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t st,
+                           Actual... args) {
+  cudaLaunchAttribute chained{};
+  chained.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  chained.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &chained;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+  count_launches(1);
+  return e;
+}
+
 template <typename T>
 __device__ __forceinline__ T from_f32(float v);
 template <>

@@ -43,9 +43,9 @@ TokenSplit token_split(int nvec, int seg) {
 }
 
 // Vectors that a lane takes of a segment: narrow ones (rows that are not
-// 16-byte aligned) in fours, to keep as many bytes in flight.
+// 16-byte aligned) several at a time, to keep more bytes in flight.
 template <typename V>
-constexpr int lane_vecs() { return sizeof(V) >= 8 ? 1 : 4; }
+constexpr int lane_vecs() { return sizeof(V) >= 8 ? 1 : sizeof(V) == 4 ? 4 : 6; }
 
 // One warp: a segment of a token's row is read once and written to the
 // token's k rows.
@@ -54,6 +54,8 @@ __global__ void __launch_bounds__(kWarps * 32)
 permute_kernel(const V* __restrict__ x, const int* __restrict__ inv, int T, int k, int nvec, int wpt,
                V* __restrict__ xp, WsHeader* hdr) {
   constexpr int kU = lane_vecs<V>(), kSeg = 32 * kU;
+  chain_go();
+  chain_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int t = blockIdx.x * (kWarps / wpt) + warp / wpt;
   if (t >= T) return;
@@ -122,6 +124,8 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
 unpermute_kernel(const Pack<T, N>* __restrict__ y, const int* __restrict__ inv, const float* __restrict__ w, int tokens,
                  int k, int nvec, int wpt, Pack<T, N>* __restrict__ out, WsHeader* hdr) {
   constexpr int kU = lane_vecs<Pack<T, N>>(), kSeg = 32 * kU;
+  chain_go();
+  chain_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int t = blockIdx.x * (kWarps / wpt) + warp / wpt;
   if (t >= tokens) return;
@@ -142,7 +146,8 @@ unpermute_kernel(const Pack<T, N>* __restrict__ y, const int* __restrict__ inv, 
       if (kWeighted && has) wm = w[p0 + j0 + lane];
       const int n = min(32, k - j0);
       int j = 0;
-      for (; j + 5 <= n; j += 5) add_rows<T, N, kU, 5, kWeighted>(y, mine, wm, j, nvec, c, acc);
+      constexpr int kB = kU == 1 ? 5 : kU == 4 ? 3 : 2;  // as the registers of 32 warps per SM allow
+      for (; j + kB <= n; j += kB) add_rows<T, N, kU, kB, kWeighted>(y, mine, wm, j, nvec, c, acc);
       for (; j + 2 <= n; j += 2) add_rows<T, N, kU, 2, kWeighted>(y, mine, wm, j, nvec, c, acc);
       if (j < n) add_rows<T, N, kU, 1, kWeighted>(y, mine, wm, j, nvec, c, acc);
     }
@@ -165,6 +170,8 @@ unpermute_grad_kernel(const Pack<T, N>* __restrict__ dout, const Pack<T, N>* __r
                       Pack<T, N>* __restrict__ dy, float* __restrict__ dw, WsHeader* hdr) {
   constexpr int kUnroll = kPW > 1 ? 1 : N * sizeof(T) == 16 ? 4 : 8;
   __shared__ float part[kWarps];
+  chain_go();
+  chain_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long p = (long long)blockIdx.x * (kWarps / kPW) + warp / kPW;
   float sum = 0.f;
@@ -227,19 +234,13 @@ int vector_bytes(size_t row_bytes, const void* a, const void* b, const void* c, 
   return int(all & 15 ? all & (~all + 1) & 15 : 16);
 }
 
-cudaError_t done() {
-  count_launches(1);
-  return cudaGetLastError();
-}
-
 template <typename V>
 cudaError_t run_permute(const void* x, const int* inv, int T, int k, size_t row_bytes, void* xp, WsHeader* hdr,
                         cudaStream_t st) {
   const int nvec = int(row_bytes / sizeof(V));
   const TokenSplit s = token_split(nvec, 32 * lane_vecs<V>());
-  permute_kernel<V><<<s.grid(T), kWarps * 32, 0, st>>>(static_cast<const V*>(x), inv, T, k, nvec, s.wpt,
-                                                            static_cast<V*>(xp), hdr);
-  return done();
+  return launch_chained(permute_kernel<V>, s.grid(T), kWarps * 32, 0, st, static_cast<const V*>(x), inv, T, k, nvec,
+                        s.wpt, static_cast<V*>(xp), hdr);
 }
 
 template <typename T, int N>
@@ -248,13 +249,8 @@ cudaError_t run_unpermute(const void* y, const int* inv, const float* w, int tok
   using V = Pack<T, N>;
   const int nvec = H / N;
   const TokenSplit s = token_split(nvec, 32 * lane_vecs<V>());
-  if (w)
-    unpermute_kernel<T, N, true><<<s.grid(tokens), kWarps * 32, 0, st>>>(
-        static_cast<const V*>(y), inv, w, tokens, k, nvec, s.wpt, static_cast<V*>(out), hdr);
-  else
-    unpermute_kernel<T, N, false><<<s.grid(tokens), kWarps * 32, 0, st>>>(
-        static_cast<const V*>(y), inv, nullptr, tokens, k, nvec, s.wpt, static_cast<V*>(out), hdr);
-  return done();
+  return launch_chained(w ? unpermute_kernel<T, N, true> : unpermute_kernel<T, N, false>, s.grid(tokens), kWarps * 32, 0,
+                        st, static_cast<const V*>(y), inv, w, tokens, k, nvec, s.wpt, static_cast<V*>(out), hdr);
 }
 
 template <typename T, int N>
@@ -263,13 +259,11 @@ cudaError_t run_unpermute_grad(const void* dout, const void* y, const int* inv, 
   using V = Pack<T, N>;
   const long long pairs = (long long)tokens * k;
   // few pairs: a block per pair, so that a row is read by eight warps at once
-  if (pairs < 1184)
-    unpermute_grad_kernel<T, N, kWarps><<<unsigned(pairs), kWarps * 32, 0, st>>>(
-        static_cast<const V*>(dout), static_cast<const V*>(y), inv, w, pairs, k, H / N, static_cast<V*>(dy), dw, hdr);
-  else
-    unpermute_grad_kernel<T, N, 1><<<unsigned((pairs + kWarps - 1) / kWarps), kWarps * 32, 0, st>>>(
-        static_cast<const V*>(dout), static_cast<const V*>(y), inv, w, pairs, k, H / N, static_cast<V*>(dy), dw, hdr);
-  return done();
+  const bool few = pairs < 1184;
+  return launch_chained(few ? unpermute_grad_kernel<T, N, kWarps> : unpermute_grad_kernel<T, N, 1>,
+                        dim3(unsigned(few ? pairs : (pairs + kWarps - 1) / kWarps)), kWarps * 32, 0, st,
+                        static_cast<const V*>(dout), static_cast<const V*>(y), inv, w, pairs, k, H / N,
+                        static_cast<V*>(dy), dw, hdr);
 }
 
 // f<T, N> for the element type and the vector width that fits.
