@@ -89,7 +89,7 @@ struct Args {
 
 // Tensor maps: codes and scales of the weights and of the tokens.
 struct Maps {
-  CUtensorMap wcodes, tcodes, wscales, tscales;
+  CUtensorMap wcodes, tcodes, tall, wscales, tscales;  // tcodes in boxes of kBoxRows rows, tall of a whole tile's
 };
 
 struct alignas(16) Tile {
@@ -143,6 +143,7 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
   } else if (warp == 2 && lane == 0) {
     ptx::tma_prefetch_map(&maps.wcodes);
     ptx::tma_prefetch_map(&maps.tcodes);
+    if (!C::kNarrow) ptx::tma_prefetch_map(&maps.tall);
     ptx::tma_prefetch_map(&maps.wscales);
     ptx::tma_prefetch_map(&maps.tscales);
   }
@@ -292,8 +293,11 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
       // ------------------------------------------------ codes
       for (int i = 0; i < n; ++i) {
         const Tile ti = list_sh[i];
-        const int boxes = (ti.rows + kBoxRows - 1) / kBoxRows;
-        const uint32_t bytes = uint32_t(C::kABytes + boxes * kBoxRows * kBKBytes);
+        // a copy takes this thread about 70 cycles: one for a tile that is nearly full
+        const bool whole = !C::kNarrow && ti.rows > kTN - kBoxRows;
+        const int boxes = whole ? 1 : (ti.rows + kBoxRows - 1) / kBoxRows;
+        const uint32_t bytes = uint32_t(C::kABytes + (whole ? kTN : boxes * kBoxRows) * kBKBytes);
+        const CUtensorMap* tmap = whole ? &maps.tall : &maps.tcodes;
         int kb = 0;
         for (; kb < KB; ++kb) {
           if (!ptx::mbar_wait(ptx::smem_addr(&empty_bar[s]), ph ^ 1u, abort_p)) break;
@@ -301,8 +305,7 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
           ptx::mbar_arrive_expect_tx(bar, bytes);
           ptx::tma_load_3d(dst, &maps.wcodes, kb * kBKBytes, ti.m0, ti.e, bar);
           for (int b = 0; b < boxes; ++b)
-            ptx::tma_load_2d(dst + C::kABytes + b * kBoxRows * kBKBytes, &maps.tcodes, kb * kBKBytes,
-                             ti.row0 + b * kBoxRows, bar);
+            ptx::tma_load_2d(dst + C::kABytes + b * kBoxRows * kBKBytes, tmap, kb * kBKBytes, ti.row0 + b * kBoxRows, bar);
           issued = min(issued + 1, kStages);
           if (++s == kStages) {
             s = 0;
@@ -638,6 +641,11 @@ bool byte_map(CUtensorMap* map, const uint8_t* base, uint64_t row_bytes, uint64_
            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Tokens per tile. Few rows per expert (at most 32 on average): narrow tiles,
+// two CTAs per SM, so that one's weights stream while the other computes.
+constexpr int kNarrowTN = 32, kWideTN = 160;
+bool narrow_tiles(int R, int E) { return R <= 32LL * E; }
+
 int sm_count() {
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -660,10 +668,8 @@ cudaError_t run(const Maps& m, const Args& a, cudaStream_t st) {
 
 template <bool kNv, typename OT>
 cudaError_t run_tiles(const Maps& m, const Args& a, cudaStream_t st) {
-  // few rows per expert: narrow tiles leave room for a ring twice as deep, and
-  // the weights stream through it
-  if (a.R <= 32LL * a.E) return run<kNv, 32, 3, 3, OT>(m, a, st);
-  return run<kNv, 160, 4, 3, OT>(m, a, st);
+  if (narrow_tiles(a.R, a.E)) return run<kNv, kNarrowTN, 3, 3, OT>(m, a, st);
+  return run<kNv, kWideTN, 4, 3, OT>(m, a, st);
 }
 
 template <bool kNv>
@@ -706,6 +712,7 @@ extern "C" moe_status moe_mxfp_matmul(const uint8_t* a_codes, const uint8_t* a_s
   const int S = scale_stride(format == MOE_FP_NV, K);
   if (!byte_map(&m.wcodes, b_codes, K / 2, N, E, 3, kBKBytes, kBM) ||
       !byte_map(&m.tcodes, a_codes, K / 2, R, 1, 2, kBKBytes, kBoxRows) ||
+      (!narrow_tiles(R, E) && !byte_map(&m.tall, a_codes, K / 2, R, 1, 2, kBKBytes, kWideTN)) ||
       !byte_map(&m.wscales, b_scales, S, N, E, 3, kSlotRow, kBM) ||
       !byte_map(&m.tscales, a_scales, S, R, 1, 2, kSlotRow, kBoxRows))
     return MOE_ERR_CUDA;
