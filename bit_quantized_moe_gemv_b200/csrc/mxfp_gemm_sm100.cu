@@ -8,8 +8,8 @@
 // sums stay in fp32 in TMEM until the one rounding of the epilogue.
 //
 // One persistent CTA per SM, 16 warps:
-//   warp 0       codes: TMA tiles of 128 bytes (256 elements of K) per row,
-//                128-byte swizzle, kStages deep
+//   warps 0, 3   codes of the weights, of the tokens: TMA tiles of 128 bytes
+//                (256 elements of K) per row, 128-byte swizzle, kStages deep
 //   warp 1       MMA issuer: the scale words of 16 bytes of each row from
 //                shared memory to TMEM (tcgen05.cp, in the MMAs' own queue), then
 //                four K = 64 MMAs per stage
@@ -122,7 +122,7 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
 
   if (warp == 0 && lane == 0) {
     for (int s = 0; s < kStages; ++s) {
-      ptx::mbar_init(ptx::smem_addr(&full_bar[s]), 1);
+      ptx::mbar_init(ptx::smem_addr(&full_bar[s]), 2);
       ptx::mbar_init(ptx::smem_addr(&empty_bar[s]), 1);
     }
     for (int s = 0; s < kSlots; ++s) {
@@ -289,28 +289,34 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
     else if (int(threadIdx.x) < n)
       list_sh[threadIdx.x] = tile_at(int(blockIdx.x) + (first_tile + int(threadIdx.x)) * int(gridDim.x));
     __syncthreads();
-    if (warp == 0 && ptx::elect_one()) {
-      // ------------------------------------------------ codes
+    if ((warp == 0 || warp == 3) && ptx::elect_one()) {
+      // ------------------------------------------------ codes: weights, tokens
+      // A copy takes its thread about 70 cycles, hence two threads and, for a
+      // token tile that is nearly full, one copy.
+      bool ready = false;
       for (int i = 0; i < n; ++i) {
         const Tile ti = list_sh[i];
-        // a copy takes this thread about 70 cycles: one for a tile that is nearly full
         const bool whole = !C::kNarrow && ti.rows > kTN - kBoxRows;
         const int boxes = whole ? 1 : (ti.rows + kBoxRows - 1) / kBoxRows;
-        const uint32_t bytes = uint32_t(C::kABytes + (whole ? kTN : boxes * kBoxRows) * kBKBytes);
+        const uint32_t bytes = warp == 0 ? C::kABytes : (whole ? kTN : boxes * kBoxRows) * kBKBytes;
         const CUtensorMap* tmap = whole ? &maps.tall : &maps.tcodes;
         int kb = 0;
         for (; kb < KB; ++kb) {
-          if (!ptx::mbar_wait(ptx::smem_addr(&empty_bar[s]), ph ^ 1u, abort_p)) break;
+          if (!ready && !ptx::mbar_wait(ptx::smem_addr(&empty_bar[s]), ph ^ 1u, abort_p)) break;
           const uint32_t bar = ptx::smem_addr(&full_bar[s]), dst = stage(s);
           ptx::mbar_arrive_expect_tx(bar, bytes);
-          ptx::tma_load_3d(dst, &maps.wcodes, kb * kBKBytes, ti.m0, ti.e, bar);
-          for (int b = 0; b < boxes; ++b)
-            ptx::tma_load_2d(dst + C::kABytes + b * kBoxRows * kBKBytes, tmap, kb * kBKBytes, ti.row0 + b * kBoxRows, bar);
+          if (warp == 0)
+            ptx::tma_load_3d(dst, &maps.wcodes, kb * kBKBytes, ti.m0, ti.e, bar);
+          else
+            for (int b = 0; b < boxes; ++b)
+              ptx::tma_load_2d(dst + C::kABytes + b * kBoxRows * kBKBytes, tmap, kb * kBKBytes, ti.row0 + b * kBoxRows,
+                               bar);
           issued = min(issued + 1, kStages);
           if (++s == kStages) {
             s = 0;
             ph ^= 1u;
           }
+          ready = ptx::mbar_test_wait(ptx::smem_addr(&empty_bar[s]), ph ^ 1u);
         }
         if (kb < KB) {
           fail(7000001);
@@ -567,7 +573,7 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
         if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&acce_bar[it & 1]));
       }
     }
-    if (warp < 3) {  // the elected lane's state, whichever lane is elected next
+    if (warp < 4) {  // the elected lane's state, whichever lane is elected next
       const int from = ptx::elected_lane();
       s = __shfl_sync(0xffffffffu, s, from);
       ph = __shfl_sync(0xffffffffu, ph, from);
@@ -585,7 +591,7 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
   if (warp == 1 && ptx::elect_one()) {
     ptx::mma_commit(ptx::smem_addr(&drain_bar));
     ptx::mbar_wait(ptx::smem_addr(&drain_bar), 0, nullptr);
-  } else if (warp == 0) {
+  } else if (warp == 0) {  // a stage is full when both warps' copies are there
     for (int i = 0; i < issued; ++i) {
       if (--s < 0) {
         s = kStages - 1;
@@ -669,7 +675,7 @@ cudaError_t run(const Maps& m, const Args& a, cudaStream_t st) {
 template <bool kNv, typename OT>
 cudaError_t run_tiles(const Maps& m, const Args& a, cudaStream_t st) {
   if (narrow_tiles(a.R, a.E)) return run<kNv, kNarrowTN, 3, 3, OT>(m, a, st);
-  return run<kNv, kWideTN, 4, 3, OT>(m, a, st);
+  return run<kNv, kWideTN, 4, 4, OT>(m, a, st);
 }
 
 template <bool kNv>
