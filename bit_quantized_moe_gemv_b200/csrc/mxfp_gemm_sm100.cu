@@ -7,7 +7,7 @@
 // the MMA (kind::mxf4 for MX, kind::mxf4nvf4 for NV); products are exact and
 // sums stay in fp32 in TMEM until the one rounding of the epilogue.
 //
-// One persistent CTA per SM, 16 warps:
+// One persistent CTA per SM (two for narrow tiles), 16 warps:
 //   warps 0, 3   codes of the weights, of the tokens: TMA tiles of 128 bytes
 //                (256 elements of K) per row, 128-byte swizzle, kStages deep
 //   warp 1       MMA issuer: the scale words of 16 bytes of each row from
@@ -21,18 +21,27 @@
 //   warps 8-15   epilogue: TMEM -> registers -> smem (transposed) -> global,
 //                on the other of two accumulators
 // The scale words could go straight to TMEM from the warps' registers, but
-// those stores and the MMAs get in each other's way: 8192^3 MX 326 us, with
-// tcgen05.cp SPEED_CP us (the MMAs alone take 141).
+// those stores and the MMAs get in each other's way: 8192^3 MX in 326 us, in
+// 295 with tcgen05.cp. One thread that waits, copies and multiplies is the next
+// limit, then the threads that issue the TMA copies (about 70 cycles each):
+// 238 us now (MX; NV 256), of which the MMAs alone take 141.
 //
 // Tiles: every CTA sums up the experts' token tiles (offsets are on the
 // device) and takes tiles b, b + grid, ... of the list "token tile, 128 weight
 // rows": neighbours share the tokens. Token tiles of experts with several of
 // them, bound by L2 and the tensor core, alternate with those of experts with
-// one, bound by HBM (8K tokens with Zipf routing, SPEED_ORDER us in the
-// experts' order); each kind keeps the experts' order, so that an expert's
-// weights are read from HBM once and its later token tiles hit L2. What a tile is (expert, rows) is
-// worked out by all threads at once for the next kListed tiles of the CTA: the
-// search and the divisions cost a single warp about 900 cycles a tile.
+// one, bound by HBM (8K tokens, 512 experts with Zipf routing: 242 us, 249 in
+// the experts' order); each kind keeps the experts' order, so that an expert's
+// weights are read from HBM once and its later token tiles hit L2. What a tile
+// is (expert, rows) is worked out by all threads at once for the next kListed
+// tiles of the CTA: the search and the divisions cost one warp about 900 cycles
+// a tile.
+//
+// Bound: HBM where an expert has up to about 160 rows (512 experts of 160 rows,
+// gate and up: 193 us, 96 % of the measured copy rate; of 16 rows: 154 us), the
+// L2 traffic of the weights beyond (2.4 GB at 10 TB/s in the Zipf case), the
+// start of a CTA (barriers, list, first copies: about 3 us) for a token's ten
+// experts (9.5 us, 2.6 us of them HBM time).
 #include <cuda.h>
 
 #include <atomic>
@@ -194,13 +203,21 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
   for (int i = 0; i < kPer; ++i) {
     const int e = threadIdx.x * kPer + i;
     first_of[i] = base1;
-    if (!C::kNarrow && e <= a.E) {
+    if (!C::kNarrow && e < a.E) {
       off_sh[e] = row_at[i];
       first_sh[0][e] = base1;
       first_sh[1][e] = base2;
     }
-    if (C::kNarrow && e == a.E) all_sh = base1;
     (!C::kNarrow && cnt[i] > 1 ? base2 : base1) += cnt[i];
+    if (e == a.E - 1) {  // the end behind the last expert
+      if (C::kNarrow) {
+        all_sh = base1;
+      } else {
+        off_sh[a.E] = row_at[i + 1];
+        first_sh[0][a.E] = base1;
+        first_sh[1][a.E] = base2;
+      }
+    }
   }
   if (!ok && threadIdx.x == 0) flag_error(a.hdr, MOE_ERR_DEVICE_FAULT, -1);
   ptx::tc_fence_before();
@@ -277,8 +294,7 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
 
   // State that a role carries from one list of tiles to the next: its place in
   // its ring and that place's phase, the same of the scale slots and the TMEM
-  // scale buffers, tiles done, copies it may have in flight (all rings full: no
-  // more than their depth).
+  // scale buffers, tiles done, copies it may have in flight.
   int s = 0, ss = 0, wb = 0, it = 0, issued = 0;
   uint32_t ph = 0, sph = 0;
 
@@ -591,7 +607,7 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
   if (warp == 1 && ptx::elect_one()) {
     ptx::mma_commit(ptx::smem_addr(&drain_bar));
     ptx::mbar_wait(ptx::smem_addr(&drain_bar), 0, nullptr);
-  } else if (warp == 0) {  // a stage is full when both warps' copies are there
+  } else if (warp == 0 || warp == 3) {  // a stage is full when both warps' copies are there
     for (int i = 0; i < issued; ++i) {
       if (--s < 0) {
         s = kStages - 1;

@@ -78,6 +78,23 @@ def test_group_sizes(sizes, fmt):
 
 
 @pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("E,rows", [(1024, 1), (1023, 2), (1024, 33), (512, 33), (513, 1)])
+def test_as_many_groups_as_there_may_be(E, rows, fmt):
+    sizes = [rows] * E
+    sizes[0], sizes[E - 1] = 5 * rows, 3 * rows  # the list's ends
+    _case(sizes, 72, 96, fmt, torch.float32, E)
+    _case([0] * (E - 1) + [40 * rows], 72, 96, fmt, torch.bfloat16, E)
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+def test_more_tiles_than_are_listed_at_once(fmt):
+    """Over 256 tiles per CTA (128 of narrow ones): the list is written again,
+    the rings go on where they were."""
+    for rows in (32, 33):  # narrow, wide
+        _case([rows], 128 * 38000 + 8, 32, fmt, torch.bfloat16, rows)
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
 def test_rows_before_and_behind_the_groups_are_left(fmt):
     _case([3, 4], 136, 256, fmt, torch.float32, 1, lead=5, behind=70)
     _case([300, 4], 136, 256, fmt, torch.bfloat16, 2, lead=9, behind=33)
