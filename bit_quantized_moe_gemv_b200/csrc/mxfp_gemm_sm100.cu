@@ -57,8 +57,7 @@ namespace {
 constexpr int kBM = 128;       // weight rows per tile
 constexpr int kBKBytes = 128;  // code bytes of a row per stage: 256 elements
 constexpr int kBoxRows = 32;   // token rows per TMA box
-constexpr int kThreads = 512;
-constexpr int kEpiWarps = 8, kScaleWarps = 3;
+constexpr int kScaleWarps = 3;
 constexpr int kSlotRow = 32;   // scale bytes of a row per slot
 constexpr int kScratch = 2048;  // epilogue staging per warp: 32 weight rows of 32 (16 bits) or 16 tokens
 
@@ -66,6 +65,7 @@ constexpr int kScratch = 2048;  // epilogue staging per warp: 32 weight rows of 
 template <int kTN, int kStages, int kSlots>
 struct Cfg {
   static constexpr bool kNarrow = kTN <= 32;  // two CTAs per SM
+  static constexpr int kEpiWarps = kNarrow ? 4 : 8, kThreads = 32 * (8 + kEpiWarps);
   static constexpr int kListed = kNarrow ? 128 : 256;  // tiles listed at a time
   static constexpr int kHalves = (kTN + 127) / 128;  // 128-row scale blocks of the token side
   static constexpr int kABytes = kBM * kBKBytes;
@@ -109,9 +109,10 @@ struct alignas(16) Tile {
 __device__ __forceinline__ int token_tiles(int rows, int tn) { return (rows + tn - 1) / tn; }
 
 template <bool kNv, int kTN, int kStages, int kSlots, typename OT>
-__global__ void __launch_bounds__(kThreads, Cfg<kTN, kStages, kSlots>::kNarrow ? 2 : 1)
+__global__ void __launch_bounds__(Cfg<kTN, kStages, kSlots>::kThreads, Cfg<kTN, kStages, kSlots>::kNarrow ? 2 : 1)
 fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
   using C = Cfg<kTN, kStages, kSlots>;
+  constexpr int kThreads = C::kThreads, kEpiWarps = C::kEpiWarps;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ __align__(8) uint64_t full_bar[kStages], empty_bar[kStages];                      // codes
@@ -541,7 +542,8 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
       constexpr int kPieces = 2 * sizeof(OT);                      // 16-byte pieces of a token's 32 values
       constexpr int kPerPiece = 16 / sizeof(OT);
       const int q = warp & 3;             // TMEM lane quarter this warp may read
-      const int half = (warp - 8) >> 2;   // two warps per quarter take turns
+      const int half = (warp - 8) >> 2;   // the warps of a quarter take turns
+      constexpr int kTurns = kEpiWarps / 4;
       uint8_t* scratch = smem + C::kScratchAt + (warp - 8) * kScratch;
       OT* out = static_cast<OT*>(a.out);
       const float ga = a.a_tscale ? *a.a_tscale : 1.f;
@@ -555,7 +557,7 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
         }
         ptx::tc_fence_after();
         const uint32_t taddr = tmem + (uint32_t(32 * q) << 16) + uint32_t((it & 1) * kTN);
-        for (int c0 = kTok * half; c0 < ti.rows; c0 += 2 * kTok) {
+        for (int c0 = kTok * half; c0 < ti.rows; c0 += kTurns * kTok) {
           uint32_t v[kTok];
           if constexpr (kTok == 32)
             ptx::tmem_ld32(taddr + uint32_t(c0), v);
@@ -685,7 +687,7 @@ cudaError_t run(const Maps& m, const Args& a, cudaStream_t st) {
   // at most this many tiles: every group with rows may end in a partial one
   const long long most = ((long long)a.R / kTN + (a.R < a.E ? a.R : a.E) + 1) * ((a.N + kBM - 1) / kBM);
   const int sms = sm_count() * (C::kNarrow ? 2 : 1);
-  return launch_chained(kernel, dim3(unsigned(most < sms ? most : sms)), kThreads, C::kSmem, st, m, a);
+  return launch_chained(kernel, dim3(unsigned(most < sms ? most : sms)), C::kThreads, C::kSmem, st, m, a);
 }
 
 template <bool kNv, typename OT>
