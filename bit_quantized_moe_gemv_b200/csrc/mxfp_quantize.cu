@@ -15,9 +15,12 @@
 // 7 bits; 64-bit arithmetic for the SwiGLU input). Approximate reciprocals and
 // exponentials are therefore enough in the common path.
 //
-// HBM bound: 8 elements per thread by 16-byte loads, a block's 4 (MX) or 2
-// (NV) lanes exchange their maxima by shuffles, codes leave as one 32-bit word
-// per thread.
+// 8 elements per thread by 16-byte loads, a block's 4 (MX) or 2 (NV) lanes
+// exchange their maxima by shuffles, codes leave as one 32-bit word per thread.
+// Dequantising is bound by HBM (63 M values to bf16: 27 us, 5.8 TB/s).
+// Quantising reads at HBM speed only in part: 63 M SwiGLU values of bf16 halves
+// in 66 us (67 % of the copy rate) and 17 M bf16 values to NV in 12 us (55 %)
+// issue 30 and 15 instructions per element, and the ALU pipe is the busiest.
 #include <cuda_fp4.h>
 #include <cuda_fp8.h>
 
@@ -238,7 +241,7 @@ __device__ __forceinline__ void quantise8(const Eight<T>& v, const Eight<T>& u, 
     }
   }
   if (kSwiglu) {
-    uint32_t m = 0;  // as integers: max takes the magnitude of one operand for free only where it need not keep NaN
+    uint32_t m = 0;  // as integers, which order like the magnitudes, NaN above infinity
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(h[i]) & 0x7fffffffu);
     top = __uint_as_float(m);

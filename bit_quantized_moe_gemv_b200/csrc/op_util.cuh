@@ -39,8 +39,8 @@ inline int dtype_size(int32_t dtype) {
 // stream still runs, and touches no memory before chain_wait, which returns
 // when the predecessor is done and its writes are seen. A predecessor of this
 // kind lets it start at chain_go, any other at its end. What runs before the
-// wait (barriers, TMEM, descriptors) and the launch itself then cost nothing: a
-// chain of small calls takes the host's 3 to 4 us each instead of 4.1 to 5.
+// wait (barriers, TMEM, descriptors) and the launch itself then overlap the
+// predecessor: two small calls in a row take 5.5 us instead of 8.2.
 __device__ __forceinline__ void chain_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void chain_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
