@@ -33,10 +33,10 @@ namespace {
 
 constexpr int kThreads = 256;
 // How far, in units of 2^-23 of its value, a computed quotient may be from the
-// exact one. Plain NV: scale product and reciprocal (1 each), products (0.5).
-// SwiGLU adds the approximate exp (the rounding of gate * log2(e), whose value
-// is below 128, gives 0.35 * 128; ex2 itself 2), the sum, the reciprocal and
-// two products (2.5). The bounds are rounded up by half.
+// exact one. Plain NV: scale product 0.5, reciprocal 1, two products 1, the
+// shift itself 0.5. SwiGLU adds the approximate exp (gate * log2(e) is below 128
+// here: its rounding gives 0.35 x 128, that of the constant 10; ex2 itself 2),
+// the sum, the reciprocal and two products (2.5): 63.
 constexpr float kOffPlain = 4.f * 0x1p-23f, kOffSwiglu = 80.f * 0x1p-23f;
 // Beyond this sum of exponentials a reciprocal may have left the normal range.
 constexpr float kExpSum = 0x1p120f;
