@@ -37,7 +37,7 @@ struct TokenSplit {
   int wpt, nseg;
   dim3 grid(int T) const {
     const int tokens = kWarps / wpt, y = (nseg + wpt - 1) / wpt;
-    return dim3(unsigned((T + tokens - 1) / tokens), unsigned(y < 65535 ? y : 65535));
+    return dim3(unsigned(((long long)T + tokens - 1) / tokens), unsigned(y < 65535 ? y : 65535));
   }
 };
 TokenSplit token_split(int nvec, int seg) {
