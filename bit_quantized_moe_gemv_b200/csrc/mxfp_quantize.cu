@@ -319,8 +319,8 @@ WarpSplit warp_split(long long rows, int per_row, int unroll) {
 
 template <typename T, bool kNv, bool kSwiglu, int kUnroll>
 __global__ void __launch_bounds__(kThreads, 4)
-quantize_kernel(const T* __restrict__ x, long long rows, WarpSplit ws, int scale_stride,
-                const float* __restrict__ tscale, const int* __restrict__ rows_dev, uint32_t* __restrict__ codes,
+quantize_kernel(const T* x, long long rows, WarpSplit ws, int scale_stride,
+                const float* tscale, const int* rows_dev, uint32_t* __restrict__ codes,
                 uint8_t* __restrict__ scales) {
   constexpr int kLanes = kNv ? 2 : 4;
   chain_go();
@@ -368,8 +368,8 @@ quantize_kernel(const T* __restrict__ x, long long rows, WarpSplit ws, int scale
 // lanes read the same), 16-byte stores.
 template <typename T, bool kNv, int kUnroll>
 __global__ void __launch_bounds__(kThreads)
-dequantize_kernel(const uint32_t* __restrict__ codes, const uint8_t* __restrict__ scales, long long rows, Split sp,
-                  int scale_stride, const float* __restrict__ tscale, const int* __restrict__ rows_dev,
+dequantize_kernel(const uint32_t* codes, const uint8_t* scales, long long rows, Split sp,
+                  int scale_stride, const float* tscale, const int* rows_dev,
                   T* __restrict__ out) {
   constexpr int kLanes = kNv ? 2 : 4;
   chain_go();

@@ -41,6 +41,9 @@ inline int dtype_size(int32_t dtype) {
 // kind lets it start at chain_go, any other at its end. What runs before the
 // wait (barriers, TMEM, descriptors) and the launch itself then overlap the
 // predecessor: two small calls in a row take 5.5 us instead of 8.2.
+// Inputs are written while the kernel is already there, so they are not
+// read-only for its lifetime: their pointers are not __restrict__ (that would
+// allow loads which need not see the predecessor's writes), the outputs' are.
 __device__ __forceinline__ void chain_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void chain_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

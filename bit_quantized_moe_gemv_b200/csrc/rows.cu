@@ -23,7 +23,7 @@ namespace {
 constexpr int kWarps = 8;
 
 // Row of pair p, or -1. A row outside [0, nrows) is reported and left out.
-__device__ __forceinline__ int pair_row(const int* __restrict__ inv, long long p, long long nrows, WsHeader* hdr) {
+__device__ __forceinline__ int pair_row(const int* inv, long long p, long long nrows, WsHeader* hdr) {
   const int r = inv[p];
   if (r >= -1 && r < nrows) return r;
   flag_error(hdr, MOE_ERR_DEVICE_FAULT, r);
@@ -56,7 +56,7 @@ constexpr int lane_vecs() { return sizeof(V) >= 8 ? 1 : sizeof(V) == 4 ? 4 : 6; 
 // token's k rows.
 template <typename V>
 __global__ void __launch_bounds__(kWarps * 32)
-permute_kernel(const V* __restrict__ x, const int* __restrict__ inv, int T, int k, int nvec, int wpt,
+permute_kernel(const V* x, const int* inv, int T, int k, int nvec, int wpt,
                V* __restrict__ xp, WsHeader* hdr) {
   constexpr int kU = lane_vecs<V>(), kSeg = 32 * kU;
   chain_go();
@@ -86,7 +86,7 @@ permute_kernel(const V* __restrict__ x, const int* __restrict__ inv, int T, int 
 
 // Adds kB rows, all loads first. Rows of -1 are left out and not read.
 template <typename T, int N, int kU, int kB, bool kWeighted>
-__device__ __forceinline__ void add_rows(const Pack<T, N>* __restrict__ y, int mine, float wmine, int j, int nvec,
+__device__ __forceinline__ void add_rows(const Pack<T, N>* y, int mine, float wmine, int j, int nvec,
                                          const int (&c)[kU], float (&acc)[kU][N]) {
   int row[kB];
   bool all = true;
@@ -126,7 +126,7 @@ __device__ __forceinline__ void add_rows(const Pack<T, N>* __restrict__ y, int m
 // One warp: a segment of out[t], the rows of several pairs in flight.
 template <typename T, int N, bool kWeighted>
 __global__ void __launch_bounds__(kWarps * 32, 4)
-unpermute_kernel(const Pack<T, N>* __restrict__ y, const int* __restrict__ inv, const float* __restrict__ w, int tokens,
+unpermute_kernel(const Pack<T, N>* y, const int* inv, const float* w, int tokens,
                  int k, int nvec, int wpt, Pack<T, N>* __restrict__ out, WsHeader* hdr) {
   constexpr int kU = lane_vecs<Pack<T, N>>(), kSeg = 32 * kU;
   chain_go();
@@ -170,8 +170,8 @@ unpermute_kernel(const Pack<T, N>* __restrict__ y, const int* __restrict__ inv, 
 // for all but a token's first pair).
 template <typename T, int N, int kPW>
 __global__ void __launch_bounds__(kWarps * 32)
-unpermute_grad_kernel(const Pack<T, N>* __restrict__ dout, const Pack<T, N>* __restrict__ y,
-                      const int* __restrict__ inv, const float* __restrict__ w, long long pairs, int k, int nvec,
+unpermute_grad_kernel(const Pack<T, N>* dout, const Pack<T, N>* y,
+                      const int* inv, const float* w, long long pairs, int k, int nvec,
                       Pack<T, N>* __restrict__ dy, float* __restrict__ dw, WsHeader* hdr) {
   constexpr int kUnroll = kPW > 1 ? 1 : N * sizeof(T) == 16 ? 4 : 8;
   __shared__ float part[kWarps];
