@@ -249,7 +249,7 @@ const char* moe_status_string(moe_status st) {
     case MOE_ERR_UNSUPPORTED: return "unsupported shape or quantisation type";
     case MOE_ERR_WORKSPACE_TOO_SMALL: return "workspace smaller than moe_workspace_size()";
     case MOE_ERR_CUDA: return "CUDA launch or copy failed";
-    case MOE_ERR_DEVICE_FAULT: return "device-side check failed (expert id out of range or bad expert descriptor)";
+    case MOE_ERR_DEVICE_FAULT: return "device-side check failed (expert id, row or offset out of range, or bad expert descriptor)";
     case MOE_ERR_TIMEOUT: return "bounded device wait expired";
     default: return "unknown status";
   }

@@ -52,7 +52,7 @@ typedef int32_t moe_status;
 #define MOE_ERR_UNSUPPORTED 2         /* shape/qtype combination not built */
 #define MOE_ERR_WORKSPACE_TOO_SMALL 3 /* ws_bytes < moe_workspace_size(...) */
 #define MOE_ERR_CUDA 4                /* a CUDA launch or copy failed */
-#define MOE_ERR_DEVICE_FAULT 5        /* device-side check failed (bad id, descriptor) */
+#define MOE_ERR_DEVICE_FAULT 5        /* device-side check failed (bad id, row, offset, descriptor) */
 #define MOE_ERR_TIMEOUT 6             /* a bounded device wait expired */
 
 /*
@@ -293,7 +293,10 @@ moe_status moe_layer_decode_noalloc(const uint16_t* x, int32_t T, int32_t H, int
  * Sums run in fp32, over j in order, and are rounded once; results do not
  * depend on scheduling. Rows of x_perm and dy_perm that no pair points to are
  * left as they were; a token without rows gets zeros, a pair without a row
- * dtopk_w 0. A row is read even where its gate is 0.
+ * dtopk_w 0. A row is read even where its gate is 0. moe_dispatch gives every
+ * pair a row of its own; pairs that share one all read it, and what is written
+ * to it (x_perm, dy_perm) is one or the other's, element by element. Outputs
+ * overlap no input.
  */
 moe_status moe_permute(const void* x, int32_t dtype, int32_t T, int32_t H, int32_t k, const int32_t* inv_perm,
                        void* x_perm, void* ws, size_t ws_bytes, void* stream);
@@ -319,8 +322,8 @@ moe_status moe_unpermute_grad(const void* dout, const void* y_perm, int32_t dtyp
  *   MOE_FP_NV  blocks of 16, scale byte E4M3, and one fp32 scale per tensor
  *              (NULL = 1) that multiplies all values; it must be a positive
  *              normal number between 2^-90 and 2^90.
- * cols is a multiple of 32, at most 2^24; codes, scales and the wide matrix are
- * 16-byte aligned.
+ * cols is a multiple of 32, at most 2^24, rows * cols at most 2^38; codes, scales
+ * and the wide matrix are 16-byte aligned. Outputs overlap no input.
  */
 #define MOE_FP_MX 1
 #define MOE_FP_NV 2
@@ -362,7 +365,9 @@ moe_status moe_mxfp_dequantize(const uint8_t* codes, const uint8_t* scales, int6
  *            MOE_ERR_DEVICE_FAULT and nothing is written.
  *   out      `out_dtype` (bf16, fp16, fp32) [R, N]; rows outside
  *            [offsets[0], offsets[E]) are left as they were
- * 0 <= R <= 2^30, 1 <= E <= 1024, 1 <= N <= 2^24, K a multiple of 32, N K < 2^41.
+ * 0 <= R <= 2^30, 1 <= E <= 1024, 1 <= N <= 2^24, R N <= 2^40, K a multiple of 32
+ * up to 2^24, N K < 2^41. A wait inside the kernel that runs out flags
+ * MOE_ERR_TIMEOUT; `out` is then undefined.
  * Sums are fp32 on the fp4 tensor cores, rounded once. A NaN scale makes every
  * result of its row (or of its weight row's column) NaN.
  */

@@ -222,3 +222,31 @@ def test_overlapping_calls_and_captured_graphs_share_a_status_workspace():
     mag = x.double().abs() * w.double().abs().sum(1, keepdim=True)
     assert ((outs[0][1].double() - ref).abs() <= _half(torch.bfloat16, ref) * (1 + 2.0 ** -10) + (k + 1) * U * mag).all()
     assert L.get_status(ws) == 0
+
+
+def test_pairs_that_share_a_row():
+    """All of them read it; what lands in it is one of theirs."""
+    from bit_quantized_moe_gemv_b200 import _lib as L
+    T, H, k = 6, 72, 3
+    inv = torch.tensor([0, 0, 1, 2, 3, 3, 0, 4, 5, 6, 6, 6, 7, 8, 2, -1, 17, 17], dtype=torch.int32, device="cuda")
+    f, ws = torch.float32, L.new_status_workspace()
+    x, y, w = _rand(T, H, dtype=f, seed=1), _rand(T * k, H, dtype=f, seed=2), _rand(T, k, dtype=f, seed=3)
+    at, has = inv.view(T, k).long().clamp(min=0), (inv.view(T, k) >= 0)[..., None]
+    terms = torch.where(has, y.double()[at], 0.0)
+    out, dy, dw, xp = torch.empty_like(x), torch.zeros_like(y), torch.empty_like(w), torch.zeros_like(y)
+    L.permute_grad(y, inv, out, ws)
+    assert ((out.double() - terms.sum(1)).abs() <= (k + 1) * U * terms.abs().sum(1)).all()
+    L.unpermute(y, inv, w, out, ws)
+    v = terms * w.double()[..., None]
+    assert ((out.double() - v.sum(1)).abs() <= (k + 1) * U * v.abs().sum(1)).all()
+    L.unpermute_grad(x, y, inv, w, dy, dw, ws)
+    v = terms * x.double()[:, None]
+    assert ((dw.double() - v.sum(2)).abs() <= H * U * v.abs().sum(2)).all()
+    L.permute(x, inv, xp, ws)
+    for r in range(T * k):
+        p = torch.nonzero(inv == r).reshape(-1)
+        if p.numel() == 0:
+            assert (xp[r] == 0).all() and (dy[r] == 0).all()
+        else:
+            assert (xp[r] == x[p // k]).any(0).all() and (dy[r] == w.view(-1)[p][:, None] * x[p // k]).any(0).all()
+    assert L.get_status(ws) == 0

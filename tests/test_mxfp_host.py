@@ -85,6 +85,8 @@ def test_fp_calls_check_their_arguments(L):
               (2, P), (7, P), (14, None), (14, ODD), (10, None)):
         assert call(md, c) == 1, c
     assert call(md, (9, 1 << 24), (4, 1 << 17)) == 1  # N K: more than a tensor map strides over
+    assert call(md, (3, 1 << 30), (9, 1025)) == 1  # R N: more tiles than are counted
+    assert call(qd, (2, (1 << 32) + 1)) == 1 and call(dd, (2, (1 << 32) + 1)) == 1  # rows * cols
     assert call(md, (11, 0)) == 2 and call(md, (13, 4)) == 2
     assert call(md, (15, 8000)) == 3
 
