@@ -10,17 +10,21 @@
 // Rounding is decided on the exact quotient, so that codes do not depend on
 // how a division was rounded: MX scales by powers of two, which is exact; in
 // the other cases the fp32 quotient is rounded twice, lowered and raised by its
-// largest error, and where the codes differ the exact comparison of x with
-// border * scale decides (an fma for plain NV, whose border * s fits
-// 7 bits; 64-bit arithmetic for the SwiGLU input). Approximate reciprocals and
-// exponentials are therefore enough in the common path.
+// largest error, and where the codes differ a comparison of x with border *
+// scale in 64 bits decides. Approximate reciprocals and exponentials are
+// therefore enough in the common path.
 //
 // 8 elements per thread by 16-byte loads, a block's 4 (MX) or 2 (NV) lanes
 // exchange their maxima by shuffles, codes leave as one 32-bit word per thread.
-// Dequantising is bound by HBM (63 M values to bf16: 27 us, 5.8 TB/s).
-// Quantising reads at HBM speed only in part: 63 M SwiGLU values of bf16 halves
-// in 66 us (67 % of the copy rate) and 17 M bf16 values to NV in 12 us (55 %)
-// issue 30 and 15 instructions per element, and the ALU pipe is the busiest.
+// Dequantising is bound by HBM (63 M values to bf16: 26 us, 6.1 TB/s).
+// Quantising comes close to it where instructions are saved: products and sums
+// two at a time, maxima three at a time, offsets that are constants (lanes side
+// by side on a row), small blocks at 56 registers, 36 warps per SM (of 64
+// registers, 32 warps: 54 us instead of 52). 63 M SwiGLU values of bf16 halves
+// take 52 us (85 % of the copy rate; 22 instructions per value, two of them
+// MUFU), 17 M bf16 values to NV 9.5 us (70 %; 13 instructions, and a fifth of
+// the time is the start of the grid). Both issue on 0.6 to 0.7 of the
+// cycles with no pipe above two thirds.
 #include <cuda_fp4.h>
 #include <cuda_fp8.h>
 
@@ -31,7 +35,7 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 // How far, in units of 2^-23 of its value, a computed quotient may be from the
 // exact one. Plain NV: scale product 0.5, reciprocal 1, two products 1, the
 // shift itself 0.5. SwiGLU adds the approximate exp (gate * log2(e) is below 128
@@ -126,6 +130,32 @@ __device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either i
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
   return y;
 }
+// Largest magnitude of three, NaN if one of them is.
+__device__ __forceinline__ float abs_max3(float a, float b, float c) {
+  float y;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+__device__ __forceinline__ float abs_max8(const float (&v)[8]) {
+  return abs_max3(abs_max3(v[0], v[1], v[2]), abs_max3(v[3], v[4], v[5]), max_nan(fabsf(v[6]), fabsf(v[7])));
+}
+// Two products or sums by one instruction, rounded as each alone.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 y;
+  asm("{\n\t.reg .b64 a, b, y;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 y, a, b;\n\tmov.b64 {%0, %1}, y;\n\t}"
+      : "=f"(y.x), "=f"(y.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return y;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 y;
+  asm("{\n\t.reg .b64 a, b, y;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 y, a, b;\n\tmov.b64 {%0, %1}, y;\n\t}"
+      : "=f"(y.x), "=f"(y.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return y;
+}
 // The value with `keep` mantissa bits nearest to v.
 __device__ __forceinline__ float border_of(float v, int keep) {
   const uint32_t low = (1u << (23 - keep)) - 1;
@@ -143,6 +173,9 @@ __device__ __forceinline__ uint32_t e2m1x2(float low, float high) {
 // sequence, so that the conversions place their bytes themselves.
 __device__ __forceinline__ uint32_t e2m1_word(const float (&h)[8], float f) {
   uint32_t w;
+  float2 q[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) q[i] = mul2(make_float2(h[2 * i], h[2 * i + 1]), make_float2(f, f));
   asm("{\n\t.reg .b8 a, b, c, d;\n\t"
       "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
       "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
@@ -150,8 +183,7 @@ __device__ __forceinline__ uint32_t e2m1_word(const float (&h)[8], float f) {
       "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
       "mov.b32 %0, {a, b, c, d};\n\t}"
       : "=r"(w)
-      : "f"(h[0] * f), "f"(h[1] * f), "f"(h[2] * f), "f"(h[3] * f), "f"(h[4] * f), "f"(h[5] * f), "f"(h[6] * f),
-        "f"(h[7] * f));
+      : "f"(q[0].x), "f"(q[0].y), "f"(q[1].x), "f"(q[1].y), "f"(q[2].x), "f"(q[2].y), "f"(q[3].x), "f"(q[3].y));
   return w;
 }
 // Largest magnitude of 8 elements, NaN if one of them is. Without their signs
@@ -166,16 +198,33 @@ __device__ __forceinline__ float abs_max(const Eight<T>& v) {
     const uint16_t b = uint16_t(max(m & 0xffffu, m >> 16));
     return std::is_same<T, __half>::value ? f16_to_f32(b) : bf16_to_f32(b);
   } else {
-    float m = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = max_nan(m, fabsf(__uint_as_float(v.p[i / 4].w[i % 4])));
-    return m;
+    float x[8];
+    v.get(x);
+    return abs_max8(x);
   }
 }
 
 // The rare exact decisions read the 8 elements again (`up` of SwiGLU inputs
 // is up_at elements behind): out of line and from memory, they cost the common
 // path neither registers nor instruction cache.
+struct Floats8 {
+  float v[8];
+};
+// silu(gate) up, for gates whose exponential overflows 32 bits.
+template <typename T>
+__device__ __noinline__ Floats8 exact_swiglu(const T* x, long long up_at) {
+  Eight<T> v, u;
+  v.load(x);
+  u.load(x + up_at);
+  float a[8], b[8];
+  v.get(a);
+  u.get(b);
+  Floats8 h;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    h.v[i] = float(a[i] < -80.f ? double(a[i]) * exp(double(a[i])) * double(b[i]) : swiglu_f64(a[i], b[i]));
+  return h;
+}
 template <typename T, bool kSwiglu>
 __device__ __noinline__ double exact_top(const T* x, long long up_at) {
   Eight<T> v, u;
@@ -225,29 +274,27 @@ __device__ __forceinline__ void quantise8(const Eight<T>& v, const Eight<T>& u, 
   float top = 0.f;
   v.get(h);
   if (kSwiglu) {
-    float up[8], exps = 0.f;
+    float up[8];
+    float2 exps = make_float2(0.f, 0.f);
     u.get(up);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float e = ex2_approx(h[i] * -1.4426950408889634f);
-      h[i] = h[i] * rcp_approx(1.f + e) * up[i];
-      exps += e;
+    for (int i = 0; i < 8; i += 2) {
+      const float2 gate = make_float2(h[i], h[i + 1]);
+      float2 e = mul2(gate, make_float2(-1.4426950408889634f, -1.4426950408889634f));
+      e = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+      exps = add2(exps, e);
+      e = add2(e, make_float2(1.f, 1.f));
+      e = mul2(mul2(gate, make_float2(rcp_approx(e.x), rcp_approx(e.y))), make_float2(up[i], up[i + 1]));
+      h[i] = e.x;
+      h[i + 1] = e.y;
     }
-    if (!(exps < kExpSum)) {
-      v.get(h);
+    if (!(exps.x + exps.y < kExpSum)) {
+      const Floats8 r = exact_swiglu<T>(x, up_at);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) h[i] = float(h[i] < -80.f ? double(h[i]) * exp(double(h[i])) * double(up[i])
-                                                            : swiglu_f64(h[i], up[i]));
+      for (int i = 0; i < 8; ++i) h[i] = r.v[i];
     }
   }
-  if (kSwiglu) {
-    uint32_t m = 0;  // as integers, which order like the magnitudes, NaN above infinity
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(h[i]) & 0x7fffffffu);
-    top = __uint_as_float(m);
-  } else {
-    top = abs_max<T>(v);
-  }
+  top = kSwiglu ? abs_max8(h) : abs_max<T>(v);
 #pragma unroll
   for (int o = 1; o < kLanes; o *= 2) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
   const bool bad = !(top <= 3.402823466e38f);  // infinite or NaN
@@ -302,66 +349,66 @@ __device__ __forceinline__ void quantise8(const Eight<T>& v, const Eight<T>& u, 
 }
 
 // How warps share the chunks of 8 elements: 2^lg lanes side by side on a row
-// (32 >> lg rows per warp), each lane with up to kUnroll chunks 2^lg apart;
-// `parts` warps make a row.
+// (32 >> lg rows per warp), each lane with up to kUnroll chunks 2^lg apart.
+// Warps of a block take consecutive rows, blockIdx.y the parts of long ones.
 struct WarpSplit {
-  int per_row, lg;
-  uint32_t parts;
-  long long warps;
+  int per_row, lg, parts;
+  long long groups;  // of 32 >> lg rows
 };
 WarpSplit warp_split(long long rows, int per_row, int unroll) {
   // as many lanes on a row as keep 9 of 10 busy; 4 lanes (a block) always do
   int lg = 5;
   while (lg > 2 && 10 * per_row < 9 * (((per_row + (1 << lg) - 1) >> lg) << lg)) --lg;
-  const uint32_t parts = uint32_t((per_row + (unroll << lg) - 1) / (unroll << lg));
-  return {per_row, lg, parts, (rows + (32 >> lg) - 1) / (32 >> lg) * parts};
+  return {per_row, lg, (per_row + (unroll << lg) - 1) / (unroll << lg), (rows + (32 >> lg) - 1) / (32 >> lg)};
 }
 
-template <typename T, bool kNv, bool kSwiglu, int kUnroll>
-__global__ void __launch_bounds__(kThreads, 4)
-quantize_kernel(const T* x, long long rows, WarpSplit ws, int scale_stride,
-                const float* tscale, const int* rows_dev, uint32_t* __restrict__ codes,
-                uint8_t* __restrict__ scales) {
+// kLg: lanes on a row, so that all offsets are constants; -1 for any.
+template <typename T, bool kNv, bool kSwiglu, int kUnroll, int kLg>
+__global__ void __launch_bounds__(kThreads, 9)
+quantize_kernel(const T* x, long long rows, int per_row, int lg, int scale_stride, const float* tscale,
+                const int* rows_dev, uint32_t* __restrict__ codes, uint8_t* __restrict__ scales) {
   constexpr int kLanes = kNv ? 2 : 4;
+  if (kLg >= 0) lg = kLg;
   chain_go();
   chain_wait();
+  const uint32_t lane = threadIdx.x % 32;
+  const long long row0 = ((long long)blockIdx.x * (kThreads / 32) + threadIdx.x / 32) << (5 - lg);
+  const long long used = rows_in_use(rows_dev, rows);
+  if (row0 >= used) return;
   const float g = kNv && tscale ? *tscale : 1.f;
   const float inv6g = 1.f / (6.f * g);
-  const uint32_t warp = blockIdx.x * (kThreads / 32) + threadIdx.x / 32, lane = threadIdx.x % 32;
-  const uint32_t group = warp / ws.parts;
-  const long long row = (long long)group * (32 >> ws.lg) + (lane >> ws.lg);
-  const int step = 1 << ws.lg;
-  const int c0 = int((warp - group * ws.parts) * kUnroll << ws.lg) + int(lane & (step - 1));
-  const int end = row < rows_in_use(rows_dev, rows) ? ws.per_row : 0;  // chunks of this lane's row
-  x += (row * (kSwiglu ? 2 : 1) * ws.per_row + c0) * 8;
-  codes += row * ws.per_row + c0;
+  const long long row = row0 + (lane >> lg);
+  const int step = 1 << lg;
+  const int c0 = int(blockIdx.y) * (kUnroll << lg) + int(lane & (step - 1));
+  const int left = row < used ? per_row - c0 : 0;  // chunks of this lane's row from c0 on
+  x += (row * (kSwiglu ? 2 : 1) * per_row + c0) * 8;
+  codes += row * per_row + c0;
   scales += row * scale_stride + c0 / kLanes;
+  const long long up_at = kSwiglu ? per_row * 8LL : 0;
   Eight<T> v[kUnroll], u[kSwiglu ? kUnroll : 1];
 #pragma unroll
   for (int i = 0; i < kUnroll; ++i) {
     v[i] = {};
     if (kSwiglu) u[i] = {};
-    if (c0 + i * step < end) {
+    if (i * step < left) {
       v[i].load(x + i * step * 8);
-      if (kSwiglu) u[i].load(x + (i * step + ws.per_row) * 8LL);
+      if (kSwiglu) u[i].load(x + i * step * 8 + up_at);
     }
   }
 #pragma unroll
   for (int i = 0; i < kUnroll; ++i) {
     uint32_t word, sc;
-    const int c = c0 + i * step;
     // all lanes: it exchanges maxima
-    quantise8<T, kNv, kSwiglu>(v[i], u[kSwiglu ? i : 0], x + i * step * 8, kSwiglu ? ws.per_row * 8LL : 0, c < end, g,
-                               inv6g, &word, &sc);
-    if (c >= end) continue;
-    codes[i * step] = word;
-    if (c % kLanes == 0) {
-      uint8_t* d = scales + i * step / kLanes;
-      *d = uint8_t(sc);
-      if (c + kLanes == end)  // the row's last block: zeros up to the stride
-        for (int k = c / kLanes + 1; k < scale_stride; ++k) *++d = 0;
+    quantise8<T, kNv, kSwiglu>(v[i], u[kSwiglu ? i : 0], x + i * step * 8, up_at, i * step < left, g, inv6g, &word,
+                               &sc);
+    if (i * step < left) {
+      codes[i * step] = word;
+      if (lane % kLanes == 0) scales[i * step / kLanes] = uint8_t(sc);
     }
   }
+  // zeros behind the row's last block, up to the stride
+  if (blockIdx.y == gridDim.y - 1 && row < used)
+    for (int k = per_row / kLanes + int(lane & (step - 1)); k < scale_stride; k += step) scales[k - c0 / kLanes] = 0;
 }
 
 // 8 elements at a time: one word of codes, one scale byte (its block's other
@@ -420,22 +467,24 @@ template <typename T, bool kNv, bool kSwiglu>
 cudaError_t run_quantize(const void* x, long long rows, int cols, const float* tscale, const int* rows_dev,
                          void* codes, uint8_t* scales, cudaStream_t st) {
   // Several chunks per lane keep enough loads in flight once the grid fills
-  // the GPU; small inputs spread wider. Lanes behind a row's end compute all
-  // the same, so three chunks where they leave fewer of those (rows of 96
-  // chunks, SwiGLU: 66 us in threes, 87 in twos).
+  // the GPU (NV of 2,048 columns: 9.7 us in fours, 10.8 in twos); small inputs
+  // spread wider. Lanes behind a row's end compute all the same, so three chunks
+  // where they leave fewer of those (rows of 96 chunks, SwiGLU: a third of the
+  // lanes' work in twos). Rows have at most 2^21 chunks, 2^15 parts.
   constexpr int kUnroll = sizeof(T) == 4 || kSwiglu ? 2 : 4;
   const T* in = static_cast<const T*>(x);
   uint32_t* out = static_cast<uint32_t*>(codes);
   const int stride = scale_stride(kNv, cols), per_row = cols / 8;
-  auto launch = [&](auto* kernel, const WarpSplit& ws) {
-    const unsigned grid = unsigned((ws.warps + kThreads / 32 - 1) / (kThreads / 32));
-    return launch_chained(kernel, dim3(grid), kThreads, 0, st, in, rows, ws, stride, tscale, rows_dev, out, scales);
+  auto launch = [&](auto* kernel, const WarpSplit& w) {
+    const dim3 grid(unsigned((w.groups + kThreads / 32 - 1) / (kThreads / 32)), unsigned(w.parts));
+    return launch_chained(kernel, grid, kThreads, 0, st, in, rows, per_row, w.lg, stride, tscale, rows_dev, out, scales);
   };
   if (rows * per_row < 148LL * 8 * kThreads * kUnroll)
-    return launch(quantize_kernel<T, kNv, kSwiglu, 1>, warp_split(rows, per_row, 1));
+    return launch(quantize_kernel<T, kNv, kSwiglu, 1, -1>, warp_split(rows, per_row, 1));
   const WarpSplit a = warp_split(rows, per_row, kUnroll), b = warp_split(rows, per_row, 3);
-  return a.parts * kUnroll <= b.parts * 3 ? launch(quantize_kernel<T, kNv, kSwiglu, kUnroll>, a)
-                                          : launch(quantize_kernel<T, kNv, kSwiglu, 3>, b);
+  if (a.parts * kUnroll <= b.parts * 3)
+    return launch(a.lg == 5 ? quantize_kernel<T, kNv, kSwiglu, kUnroll, 5> : quantize_kernel<T, kNv, kSwiglu, kUnroll, -1>, a);
+  return launch(b.lg == 5 ? quantize_kernel<T, kNv, kSwiglu, 3, 5> : quantize_kernel<T, kNv, kSwiglu, 3, -1>, b);
 }
 
 template <typename T>

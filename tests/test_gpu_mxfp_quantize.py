@@ -180,3 +180,20 @@ def test_empty_and_captured():
     want_c, want_s = ref.quantise(x, "mx")
     assert torch.equal(codes, ref.pack(want_c)) and torch.equal(scales, ref.pad_scales(want_s, 512, "mx"))
     assert torch.equal(out, ref.values(codes, scales, "mx").float())
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("cols", [32, 96, 256, 320, 480, 768, 1312])
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_large_inputs_of_every_row_split(cols, swiglu, fmt):
+    """Rows that 4, 8, 16 and 32 lanes share, in ones to fours; the used rows end
+    inside a warp's."""
+    dtype = torch.bfloat16 if cols % 64 else torch.float32
+    rows = 5_000_000 // cols + 3
+    g = torch.Generator().manual_seed(cols)
+    x = torch.randn(rows, cols * (2 if swiglu else 1), generator=g).to(dtype).cuda()
+    codes, scales = _check(x, fmt, _tscale(fmt, 0.01), swiglu)
+    n = torch.tensor([rows - 1234], dtype=torch.int32, device="cuda")
+    c, s = _quantise(x, fmt, _tscale(fmt, 0.01), swiglu, n)
+    assert torch.equal(c[:n], codes[:n]) and torch.equal(s[:n], scales[:n])
+    assert (c[n:] == 0xAB).all() and (s[n:] == 0xAB).all()
