@@ -39,9 +39,11 @@
 //
 // Bound: HBM where an expert has up to about 160 rows (512 experts of 160 rows,
 // gate and up: 193 us, 96 % of the measured copy rate; of 16 rows: 154 us), the
-// L2 traffic of the weights beyond (2.4 GB at 10 TB/s in the Zipf case), the
-// start of a CTA (barriers, list, first copies: about 3 us) for a token's ten
-// experts (9.5 us, 2.6 us of them HBM time).
+// operands' way beyond (a stage of 160 tokens brings 36 KB from L2 at 64 bytes a
+// cycle and takes 72 KB through shared memory at 128: 576 cycles either way, of
+// 628 measured at 8192^3, where its MMAs take 372), the start of a CTA (barriers,
+// list, first copies: about 3 us) for a token's ten experts (9.1 us, 2.6 us of
+// them HBM time).
 #include <cuda.h>
 
 #include <atomic>

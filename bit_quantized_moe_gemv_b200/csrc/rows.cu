@@ -12,15 +12,16 @@
 // bytes in flight: rows are loaded five at a time and kept packed until they
 // are added, so that a thread needs 64 registers and 32 warps fit an SM (116
 // registers and 14 warps with the elements taken apart: 97 us for unpermute).
-// 8,192 tokens x 2,048 bf16, ten experts: permute 60 us, permute_grad 60,
-// unpermute 62 (6.0 to 6.2 TB/s), unpermute_grad 111 (6.3 TB/s).
+// 8,192 tokens x 2,048 bf16, ten experts: permute 60 us, permute_grad 57,
+// unpermute 58 (6.2 to 6.5 TB/s), unpermute_grad 111 (6.4 TB/s).
 #include "call_range.h"
 #include "op_util.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 8;     // of a block of the gradient kernel
+constexpr int kSegWarps = 4;  // of the others: small blocks spread evenly over the SMs
 
 // Row of pair p, or -1. A row outside [0, nrows) is reported and left out.
 __device__ __forceinline__ int pair_row(const int* inv, long long p, long long nrows, WsHeader* hdr) {
@@ -30,21 +31,36 @@ __device__ __forceinline__ int pair_row(const int* inv, long long p, long long n
   return -1;
 }
 
-// A block has kWarps warps: `wpt` (a power of two) of them take consecutive
-// segments of one token's row, so kWarps / wpt tokens per block;
-// gridDim.y blocks share the segments of long rows.
-struct TokenSplit {
-  int wpt, nseg;
-  dim3 grid(int T) const {
-    const int tokens = kWarps / wpt, y = (nseg + wpt - 1) / wpt;
-    return dim3(unsigned(((long long)T + tokens - 1) / tokens), unsigned(y < 65535 ? y : 65535));
-  }
+// One warp per segment of a token's row, the segments of all rows in one line.
+// The sums take them as they are, so that no warp is without one however many a
+// row has (8,192 tokens x 1,032 16-bit values, five segments: unpermute 28 us;
+// with eight warps per row 35). permute, which waits for nothing but its own
+// stores, rounds them up to a power of two and lets the surplus warps leave
+// (1,021 tokens x 1,032: 4.2 us, as they are 4.7; no difference at 8,192).
+struct Segments {
+  int per_row, shift;  // shift: log2(per_row) or -1
+  long long all;
+  unsigned blocks() const { return unsigned((all + kSegWarps - 1) / kSegWarps); }
 };
-TokenSplit token_split(int nvec, int seg) {
-  const int nseg = (nvec + seg - 1) / seg;
-  int w = 1;
-  while (w < kWarps && w < nseg) w *= 2;
-  return {w, nseg};
+Segments row_segments(long long T, int nvec, int seg, bool rounded) {
+  const int n = (nvec + seg - 1) / seg;
+  int l = 0;
+  while ((1 << l) < n) ++l;
+  const int per_row = rounded ? 1 << l : n;
+  return {per_row, per_row == 1 << l ? l : -1, T * per_row};
+}
+// This warp's token and segment; false if there is none.
+__device__ __forceinline__ bool segment_at(const Segments& s, int* token, int* seg) {
+  const long long w = (long long)blockIdx.x * kSegWarps + (threadIdx.x >> 5);
+  if (w >= s.all) return false;
+  if (s.shift >= 0)
+    *token = int(w >> s.shift);
+  else if (s.all <= 0xffffffffLL)
+    *token = int(uint32_t(w) / uint32_t(s.per_row));
+  else
+    *token = int(w / s.per_row);
+  *seg = int(w - (long long)*token * s.per_row);
+  return true;
 }
 
 // Vectors that a lane takes of a segment: narrow ones (rows that are not
@@ -55,31 +71,29 @@ constexpr int lane_vecs() { return sizeof(V) >= 8 ? 1 : sizeof(V) == 4 ? 4 : 6; 
 // One warp: a segment of a token's row is read once and written to the
 // token's k rows.
 template <typename V>
-__global__ void __launch_bounds__(kWarps * 32)
-permute_kernel(const V* x, const int* inv, int T, int k, int nvec, int wpt,
-               V* __restrict__ xp, WsHeader* hdr) {
+__global__ void __launch_bounds__(kSegWarps * 32)
+permute_kernel(const V* x, const int* inv, long long nrows, int k, int nvec, Segments segs, V* __restrict__ xp,
+               WsHeader* hdr) {
   constexpr int kU = lane_vecs<V>(), kSeg = 32 * kU;
   chain_go();
   chain_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int t = blockIdx.x * (kWarps / wpt) + warp / wpt;
-  if (t >= T) return;
-  const long long p0 = (long long)t * k, nrows = (long long)T * k;
-  for (int s = blockIdx.y * wpt + warp % wpt; s < (nvec + kSeg - 1) / kSeg; s += gridDim.y * wpt) {
-    const int c = s * kSeg + lane;
-    V v[kU];
+  const int lane = threadIdx.x & 31;
+  int t, s;
+  if (!segment_at(segs, &t, &s) || s * kSeg >= nvec) return;
+  const long long p0 = (long long)t * k;
+  const int c = s * kSeg + lane;
+  V v[kU];
 #pragma unroll
-    for (int u = 0; u < kU; ++u) v[u] = x[(size_t)t * nvec + min(c + 32 * u, nvec - 1)];
-    for (int j0 = 0; j0 < k; j0 += 32) {
-      const int mine = j0 + lane < k ? pair_row(inv, p0 + j0 + lane, nrows, hdr) : -1;
-      const int n = min(32, k - j0);
-      for (int j = 0; j < n; ++j) {
-        const int r = __shfl_sync(0xffffffffu, mine, j);
-        if (r < 0) continue;
+  for (int u = 0; u < kU; ++u) v[u] = x[(size_t)t * nvec + min(c + 32 * u, nvec - 1)];
+  for (int j0 = 0; j0 < k; j0 += 32) {
+    const int mine = j0 + lane < k ? pair_row(inv, p0 + j0 + lane, nrows, hdr) : -1;
+    const int n = min(32, k - j0);
+    for (int j = 0; j < n; ++j) {
+      const int r = __shfl_sync(0xffffffffu, mine, j);
+      if (r < 0) continue;
 #pragma unroll
-        for (int u = 0; u < kU; ++u)
-          if (c + 32 * u < nvec) xp[(size_t)r * nvec + c + 32 * u] = v[u];
-      }
+      for (int u = 0; u < kU; ++u)
+        if (c + 32 * u < nvec) xp[(size_t)r * nvec + c + 32 * u] = v[u];
     }
   }
 }
@@ -125,43 +139,41 @@ __device__ __forceinline__ void add_rows(const Pack<T, N>* y, int mine, float wm
 
 // One warp: a segment of out[t], the rows of several pairs in flight.
 template <typename T, int N, bool kWeighted>
-__global__ void __launch_bounds__(kWarps * 32, 4)
-unpermute_kernel(const Pack<T, N>* y, const int* inv, const float* w, int tokens,
-                 int k, int nvec, int wpt, Pack<T, N>* __restrict__ out, WsHeader* hdr) {
+__global__ void __launch_bounds__(kSegWarps * 32, 8)
+unpermute_kernel(const Pack<T, N>* y, const int* inv, const float* w, long long nrows, int k, int nvec, Segments segs,
+                 Pack<T, N>* __restrict__ out, WsHeader* hdr) {
   constexpr int kU = lane_vecs<Pack<T, N>>(), kSeg = 32 * kU;
   chain_go();
   chain_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int t = blockIdx.x * (kWarps / wpt) + warp / wpt;
-  if (t >= tokens) return;
-  const long long p0 = (long long)t * k, nrows = (long long)tokens * k;
-  for (int s = blockIdx.y * wpt + warp % wpt; s < (nvec + kSeg - 1) / kSeg; s += gridDim.y * wpt) {
-    int c[kU];  // lanes behind the row's end read its last vector again
-    float acc[kU][N];
+  const int lane = threadIdx.x & 31;
+  int t, s;
+  if (!segment_at(segs, &t, &s)) return;
+  const long long p0 = (long long)t * k;
+  int c[kU];  // lanes behind the row's end read its last vector again
+  float acc[kU][N];
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      c[u] = min(s * kSeg + 32 * u + lane, nvec - 1);
+  for (int u = 0; u < kU; ++u) {
+    c[u] = min(s * kSeg + 32 * u + lane, nvec - 1);
 #pragma unroll
-      for (int i = 0; i < N; ++i) acc[u][i] = 0.f;
-    }
-    for (int j0 = 0; j0 < k; j0 += 32) {
-      const bool has = j0 + lane < k;
-      const int mine = has ? pair_row(inv, p0 + j0 + lane, nrows, hdr) : -1;
-      float wm = 1.f;
-      if (kWeighted && has) wm = w[p0 + j0 + lane];
-      const int n = min(32, k - j0);
-      int j = 0;
-      constexpr int kB = kU == 1 ? 5 : kU == 4 ? 3 : 2;  // as the registers of 32 warps per SM allow
-      for (; j + kB <= n; j += kB) add_rows<T, N, kU, kB, kWeighted>(y, mine, wm, j, nvec, c, acc);
-      for (; j + 2 <= n; j += 2) add_rows<T, N, kU, 2, kWeighted>(y, mine, wm, j, nvec, c, acc);
-      if (j < n) add_rows<T, N, kU, 1, kWeighted>(y, mine, wm, j, nvec, c, acc);
-    }
+    for (int i = 0; i < N; ++i) acc[u][i] = 0.f;
+  }
+  for (int j0 = 0; j0 < k; j0 += 32) {
+    const bool has = j0 + lane < k;
+    const int mine = has ? pair_row(inv, p0 + j0 + lane, nrows, hdr) : -1;
+    float wm = 1.f;
+    if (kWeighted && has) wm = w[p0 + j0 + lane];
+    const int n = min(32, k - j0);
+    int j = 0;
+    constexpr int kB = kU == 1 ? 5 : kU == 4 ? 3 : 2;  // as the registers of 32 warps per SM allow
+    for (; j + kB <= n; j += kB) add_rows<T, N, kU, kB, kWeighted>(y, mine, wm, j, nvec, c, acc);
+    for (; j + 2 <= n; j += 2) add_rows<T, N, kU, 2, kWeighted>(y, mine, wm, j, nvec, c, acc);
+    if (j < n) add_rows<T, N, kU, 1, kWeighted>(y, mine, wm, j, nvec, c, acc);
+  }
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      Pack<T, N> o;
-      o.set(acc[u]);
-      if (s * kSeg + 32 * u + lane < nvec) out[(size_t)t * nvec + c[u]] = o;
-    }
+  for (int u = 0; u < kU; ++u) {
+    Pack<T, N> o;
+    o.set(acc[u]);
+    if (s * kSeg + 32 * u + lane < nvec) out[(size_t)t * nvec + c[u]] = o;
   }
 }
 
@@ -243,9 +255,9 @@ template <typename V>
 cudaError_t run_permute(const void* x, const int* inv, int T, int k, size_t row_bytes, void* xp, WsHeader* hdr,
                         cudaStream_t st) {
   const int nvec = int(row_bytes / sizeof(V));
-  const TokenSplit s = token_split(nvec, 32 * lane_vecs<V>());
-  return launch_chained(permute_kernel<V>, s.grid(T), kWarps * 32, 0, st, static_cast<const V*>(x), inv, T, k, nvec,
-                        s.wpt, static_cast<V*>(xp), hdr);
+  const Segments s = row_segments(T, nvec, 32 * lane_vecs<V>(), true);
+  return launch_chained(permute_kernel<V>, dim3(s.blocks()), kSegWarps * 32, 0, st, static_cast<const V*>(x), inv,
+                        (long long)T * k, k, nvec, s, static_cast<V*>(xp), hdr);
 }
 
 template <typename T, int N>
@@ -253,9 +265,10 @@ cudaError_t run_unpermute(const void* y, const int* inv, const float* w, int tok
                           WsHeader* hdr, cudaStream_t st) {
   using V = Pack<T, N>;
   const int nvec = H / N;
-  const TokenSplit s = token_split(nvec, 32 * lane_vecs<V>());
-  return launch_chained(w ? unpermute_kernel<T, N, true> : unpermute_kernel<T, N, false>, s.grid(tokens), kWarps * 32, 0,
-                        st, static_cast<const V*>(y), inv, w, tokens, k, nvec, s.wpt, static_cast<V*>(out), hdr);
+  const Segments s = row_segments(tokens, nvec, 32 * lane_vecs<V>(), false);
+  return launch_chained(w ? unpermute_kernel<T, N, true> : unpermute_kernel<T, N, false>, dim3(s.blocks()), kSegWarps * 32,
+                        0, st, static_cast<const V*>(y), inv, w, (long long)tokens * k, k, nvec, s,
+                        static_cast<V*>(out), hdr);
 }
 
 template <typename T, int N>
@@ -314,9 +327,12 @@ cudaError_t launch_unpermute_grad(const void* dout, const void* y, int dtype, in
   MOE_DISPATCH_VEC(run_unpermute_grad, dtype, vb, dout, y, inv, w, T, k, H, dy, dw, hdr, st);
 }
 
-// Shapes of the row operators: any H, the pair index in 32 bits.
-bool rows_shape_ok(int64_t T, int64_t H, int64_t k) {
-  return T >= 0 && H >= 1 && H <= (1 << 24) && k >= 1 && k <= kMaxK && T * k <= 0x7fffffffLL;
+// Shapes of the row operators: the pair index in 32 bits, and at most 2^38 bytes
+// of rows, which keeps the blocks within a grid (a row of several segments has
+// less than four for every 192 bytes, a block four).
+bool rows_shape_ok(int64_t T, int64_t H, int64_t k, int32_t dtype) {
+  return T >= 0 && H >= 1 && H <= (1 << 24) && k >= 1 && k <= kMaxK && T * k <= 0x7fffffffLL &&
+         T * k * dtype_size(dtype) <= (1LL << 38) / H;
 }
 
 moe_status rows_check(const void* a, const void* b, int32_t dtype, bool bytes_ok, const void* inv, void* ws,
@@ -340,7 +356,7 @@ extern "C" {
 moe_status moe_permute(const void* x, int32_t dtype, int32_t T, int32_t H, int32_t k, const int32_t* inv_perm,
                        void* x_perm, void* ws, size_t ws_bytes, void* stream) {
   const CallRange range("moe_permute");
-  if (!rows_shape_ok(T, H, k)) return MOE_ERR_INVALID_ARG;
+  if (!rows_shape_ok(T, H, k, dtype)) return MOE_ERR_INVALID_ARG;
   if (T == 0) return MOE_OK;
   const moe_status s = rows_check(x, x_perm, dtype, true, inv_perm, ws, ws_bytes);
   if (s != MOE_OK) return s;
@@ -351,7 +367,7 @@ moe_status moe_permute(const void* x, int32_t dtype, int32_t T, int32_t H, int32
 moe_status moe_permute_grad(const void* dx_perm, int32_t dtype, int32_t T, int32_t H, int32_t k,
                             const int32_t* inv_perm, void* dx, void* ws, size_t ws_bytes, void* stream) {
   const CallRange range("moe_permute_grad");
-  if (!rows_shape_ok(T, H, k)) return MOE_ERR_INVALID_ARG;
+  if (!rows_shape_ok(T, H, k, dtype)) return MOE_ERR_INVALID_ARG;
   if (T == 0) return MOE_OK;
   const moe_status s = rows_check(dx_perm, dx, dtype, false, inv_perm, ws, ws_bytes);
   if (s != MOE_OK) return s;
@@ -362,7 +378,7 @@ moe_status moe_permute_grad(const void* dx_perm, int32_t dtype, int32_t T, int32
 moe_status moe_unpermute(const void* y_perm, int32_t dtype, int32_t T, int32_t H, int32_t k, const int32_t* inv_perm,
                          const float* topk_w, void* out, void* ws, size_t ws_bytes, void* stream) {
   const CallRange range("moe_unpermute");
-  if (!rows_shape_ok(T, H, k)) return MOE_ERR_INVALID_ARG;
+  if (!rows_shape_ok(T, H, k, dtype)) return MOE_ERR_INVALID_ARG;
   if (T == 0) return MOE_OK;
   const moe_status s = rows_check(y_perm, out, dtype, false, inv_perm, ws, ws_bytes);
   if (s != MOE_OK) return s;
@@ -375,7 +391,7 @@ moe_status moe_unpermute_grad(const void* dout, const void* y_perm, int32_t dtyp
                               const int32_t* inv_perm, const float* topk_w, void* dy_perm, float* dtopk_w, void* ws,
                               size_t ws_bytes, void* stream) {
   const CallRange range("moe_unpermute_grad");
-  if (!rows_shape_ok(T, H, k)) return MOE_ERR_INVALID_ARG;
+  if (!rows_shape_ok(T, H, k, dtype)) return MOE_ERR_INVALID_ARG;
   if (T == 0) return MOE_OK;
   moe_status s = rows_check(dout, dy_perm, dtype, false, inv_perm, ws, ws_bytes);
   if (s != MOE_OK) return s;

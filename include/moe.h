@@ -288,8 +288,8 @@ moe_status moe_layer_decode_noalloc(const uint16_t* x, int32_t T, int32_t H, int
  * x, dx, out, dout are [T, H], x_perm, dx_perm, y_perm, dy_perm [T*k, H], all
  * of `dtype` (moe_permute takes MOE_DT_U8 as well: rows of packed codes or
  * block scales); topk_w and dtopk_w are fp32 [T, k]. Any H in [1, 2^24],
- * 1 <= k <= 64, T*k < 2^31; pointers aligned to their elements (16-byte
- * aligned rows are fastest).
+ * 1 <= k <= 64, T*k < 2^31, [T*k, H] at most 2^38 bytes; pointers aligned to
+ * their elements (16-byte aligned rows are fastest).
  * Sums run in fp32, over j in order, and are rounded once; results do not
  * depend on scheduling. Rows of x_perm and dy_perm that no pair points to are
  * left as they were; a token without rows gets zeros, a pair without a row

@@ -95,6 +95,13 @@ def test_more_tiles_than_are_listed_at_once(fmt):
 
 
 @pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("K", [32, 256, 288, 768, 1056, 2080])
+@pytest.mark.parametrize("N,dtype", [(2048, torch.bfloat16), (2184, torch.float16), (2307, torch.float32)])
+def test_experts_with_none_one_and_many_tiles(N, dtype, K, fmt):
+    _case([1, 0, 4700, 40, 0, 161, 320, 129], N, K, fmt, dtype, N + K, lead=3, behind=5)
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
 def test_rows_before_and_behind_the_groups_are_left(fmt):
     _case([3, 4], 136, 256, fmt, torch.float32, 1, lead=5, behind=70)
     _case([300, 4], 136, 256, fmt, torch.bfloat16, 2, lead=9, behind=33)

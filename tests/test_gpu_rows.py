@@ -250,3 +250,26 @@ def test_pairs_that_share_a_row():
         else:
             assert (xp[r] == x[p // k]).any(0).all() and (dy[r] == w.view(-1)[p][:, None] * x[p // k]).any(0).all()
     assert L.get_status(ws) == 0
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("H", [1, 31, 127, 128, 129, 192, 193, 256, 260, 516, 1032, 1544])
+def test_rows_of_every_number_of_segments(H, dtype):
+    """One to many segments of a warp, powers of two and not, at tokens that end inside a block."""
+    from bit_quantized_moe_gemv_b200 import _lib as L
+    T, k, E = 203, 3, 16
+    _, inv, ws = _routing(T, k, E, H, 0.2)
+    x, y, w = _rand(T, H, dtype=dtype, seed=1), _rand(T * k, H, dtype=dtype, seed=2), _rand(T, k, dtype=torch.float32, seed=3)
+    at, has = inv.view(T, k).long().clamp(min=0), (inv.view(T, k) >= 0)[..., None]
+    xp = torch.full((T * k, H), 7, dtype=dtype, device="cuda")
+    want = xp.clone()
+    p = torch.nonzero(inv >= 0).reshape(-1)
+    want[inv[p].long()] = x[p // k]
+    L.permute(x, inv, xp, ws)
+    assert torch.equal(xp, want)
+    terms = torch.where(has, y.double()[at] * w.double()[..., None], 0.0)
+    out = torch.full((T, H), 7, dtype=dtype, device="cuda")
+    L.unpermute(y, inv, w, out, ws)
+    ref, mag = terms.sum(1), terms.abs().sum(1)
+    assert ((out.double() - ref).abs() <= _half(dtype, ref) * (1 + 2.0 ** -10) + (k + 1) * U * mag).all()
+    assert L.get_status(ws) == 0

@@ -33,7 +33,7 @@ def test_row_calls_check_their_arguments(L):
 
     assert call(_2=0) == 0  # no tokens: nothing to do
     for bad in (dict(_0=None), dict(_5=None), dict(_6=None), dict(_7=None), dict(_2=-1), dict(_3=0), dict(_3=1 << 25),
-                dict(_4=0), dict(_4=65), dict(_2=1 << 30), dict(_0=ODD), dict(_6=ODD), dict(_5=ODD), dict(_7=ODD)):
+                dict(_4=0), dict(_4=65), dict(_2=1 << 30), dict(_2=1 << 14, _3=1 << 23), dict(_0=ODD), dict(_6=ODD), dict(_5=ODD), dict(_7=ODD)):
         assert call(**bad) == 1, bad
     assert call(_1=0) == 2 and call(_1=5) == 2
     assert call(_8=8703) == 3
