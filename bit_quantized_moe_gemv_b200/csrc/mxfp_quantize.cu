@@ -325,9 +325,9 @@ __device__ __forceinline__ void quantise8(const Eight<T>& v, const Eight<T>& u, 
     inv = s > 0.f ? rcp_approx(s * g) : 0.f;
   } else {
     if (kSwiglu) {
-      // the exponent changes at a power of two (below 2^-124 the scale byte is 0 either way)
+      // the exponent changes at a power of two; the lowest that changes the scale byte (0 to 1) is 2^-124
       const uint32_t above = __float_as_uint(top * (1.f + kOff)) & 0xff800000u;
-      const bool near = !bad && __float_as_uint(top * (1.f - kOff)) < above && top > 0x1p-124f;
+      const bool near = !bad && __float_as_uint(top * (1.f - kOff)) < above && top > 0x1p-125f;
       if (__any_sync(0xffffffffu, near)) {
         const double t = top_f64();
         if (near) top = t < double(__uint_as_float(above)) ? __uint_as_float(above - 1) : __uint_as_float(above);

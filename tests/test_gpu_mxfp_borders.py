@@ -1,0 +1,46 @@
+"""SwiGLU quantisation at the ends of the fp32 range, byte for byte against
+fp64."""
+import pytest
+import torch
+
+from tests import mxfp_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+
+def _check(gate, up, fmt, g=None):
+    """gate, up [rows, cols] of one type."""
+    from bit_quantized_moe_gemv_b200 import _lib as L
+    rows, cols = gate.shape
+    x = torch.cat((gate, up), 1).contiguous().cuda()
+    codes = torch.zeros(rows, cols // 2, dtype=torch.uint8, device="cuda")
+    scales = torch.zeros(rows, L.mxfp_scale_stride(cols, fmt), dtype=torch.uint8, device="cuda")
+    L.mxfp_quantize(x, codes, scales, fmt, None if g is None else torch.tensor([g], device="cuda"), swiglu=True)
+    v = ref.swiglu(x)
+    code, byte = ref.quantise(v, fmt, 1.0 if g is None else float(torch.tensor(g)))
+    torch.testing.assert_close(scales, ref.pad_scales(byte, cols, fmt), rtol=0, atol=0)
+    torch.testing.assert_close(codes, ref.pack(code), rtol=0, atol=0)
+    return code, byte
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_block_maxima_beside_the_smallest_scales(dtype):
+    """silu(gate) up about 2^-124, where the MX byte changes from 0 to 1, and
+    about its neighbours."""
+    g = torch.Generator().manual_seed(1)
+    gates, ups = [], []
+    for e in (-127, -126, -125, -124, -123, -122):
+        for k in (3, 4, 5, 6):  # gates of 8 to 64: silu is the gate less a part in 3,000 to 2^92
+            gates.append(torch.full((32,), 2.0 ** k))
+            ups.append(torch.full((32,), 2.0 ** (e - k)))
+        for _ in range(40):
+            gate = 40 * torch.rand(32, generator=g) + 0.5
+            want = 2.0 ** e * (1 + (torch.rand(32, generator=g) - 0.5) * 2.0 ** -20)
+            silu = gate.double() / (1 + torch.exp(-gate.double()))
+            gates.append(gate)
+            ups.append((want.double() / silu).float())
+    code, byte = _check(torch.stack(gates).to(dtype), torch.stack(ups).to(dtype), "mx")
+    assert {0, 1, 2} <= set(byte.reshape(-1).tolist())
+    # silu(32) is 32 less a part in 2^46: 2^-124 is not reached
+    code, byte = _check(torch.full((1, 32), 32.0).to(dtype), torch.full((1, 32), 2.0 ** -129).to(dtype), "mx")
+    assert byte.item() == 0 and (code == 7).all()
