@@ -44,6 +44,10 @@ constexpr int kThreads = 128;
 constexpr float kOffPlain = 4.f * 0x1p-23f, kOffSwiglu = 80.f * 0x1p-23f;
 // Beyond this sum of exponentials a reciprocal may have left the normal range.
 constexpr float kExpSum = 0x1p120f;
+// Gates below this (bits of a float) are rounded away when they are halved: their
+// silu is a subnormal number, while its product with up need not be one. Only
+// fp32 has such gates: the lowest bit of a 16-bit subnormal survives.
+constexpr uint32_t kTinyGate = (127u - 120u) << 23;  // 2^-120
 
 // Rows in chunks of 8 elements: chunk g is chunk (g % per_row) of row
 // (g / per_row). For fewer than 2^31 chunks the quotient comes from one
@@ -210,7 +214,7 @@ __device__ __forceinline__ float abs_max(const Eight<T>& v) {
 struct Floats8 {
   float v[8];
 };
-// silu(gate) up, for gates whose exponential overflows 32 bits.
+// silu(gate) up, for gates whose exponential overflows 32 bits or whose silu falls below them.
 template <typename T>
 __device__ __noinline__ Floats8 exact_swiglu(const T* x, long long up_at) {
   Eight<T> v, u;
@@ -276,10 +280,13 @@ __device__ __forceinline__ void quantise8(const Eight<T>& v, const Eight<T>& u, 
   if (kSwiglu) {
     float up[8];
     float2 exps = make_float2(0.f, 0.f);
+    uint32_t least = 0xffffffffu;  // smallest gate, as twice its bits less one: no sign, zeros last
     u.get(up);
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
       const float2 gate = make_float2(h[i], h[i + 1]);
+      if (sizeof(T) == 4)
+        least = min(least, min(2 * __float_as_uint(gate.x) - 1, 2 * __float_as_uint(gate.y) - 1));
       float2 e = mul2(gate, make_float2(-1.4426950408889634f, -1.4426950408889634f));
       e = make_float2(ex2_approx(e.x), ex2_approx(e.y));
       exps = add2(exps, e);
@@ -288,7 +295,7 @@ __device__ __forceinline__ void quantise8(const Eight<T>& v, const Eight<T>& u, 
       h[i] = e.x;
       h[i + 1] = e.y;
     }
-    if (!(exps.x + exps.y < kExpSum)) {
+    if (!(exps.x + exps.y < kExpSum) || least < 2 * kTinyGate - 1) {
       const Floats8 r = exact_swiglu<T>(x, up_at);
 #pragma unroll
       for (int i = 0; i < 8; ++i) h[i] = r.v[i];

@@ -44,3 +44,20 @@ def test_block_maxima_beside_the_smallest_scales(dtype):
     # silu(32) is 32 less a part in 2^46: 2^-124 is not reached
     code, byte = _check(torch.full((1, 32), 32.0).to(dtype), torch.full((1, 32), 2.0 ** -129).to(dtype), "mx")
     assert byte.item() == 0 and (code == 7).all()
+
+
+@pytest.mark.parametrize("fmt,g", [("mx", None), ("nv", None), ("nv", 2.0 ** -88), ("nv", 2.0 ** -30)])
+def test_gates_below_the_normal_range(fmt, g):
+    """sigma(gate) gate has only the bits a subnormal number has, the values all of them."""
+    r = torch.Generator().manual_seed(2)
+    gate = torch.zeros(300, 64)
+    gate[0, :2] = torch.tensor([2.0 ** -149, 2.0 ** -147])
+    for i in range(1, 300):
+        n = torch.randint(1, 1 << int(torch.randint(1, 25, (1,), generator=r)), (64,), generator=r)
+        gate[i] = n.double().mul(2.0 ** -149).float() * (1 - 2 * torch.randint(0, 2, (64,), generator=r))
+    up = torch.exp2(torch.randint(20, 127, (300, 1), generator=r).float()).expand(-1, 64) * (torch.rand(300, 64, generator=r) + 0.5)
+    up[0] = 2.0 ** 100
+    assert (gate != 0).any(1).all()
+    code, byte = _check(gate, up, fmt, g)
+    if fmt == "mx":
+        assert code[0, :2].tolist() == [2, 6]
