@@ -48,6 +48,7 @@ constexpr float kExpSum = 0x1p120f;
 // silu is a subnormal number, while its product with up need not be one. Only
 // fp32 has such gates: the lowest bit of a 16-bit subnormal survives.
 constexpr uint32_t kTinyGate = (127u - 120u) << 23;  // 2^-120
+constexpr float kLargest = 0x1.fffffep127f, kInf = __builtin_huge_valf();
 
 // Rows in chunks of 8 elements: chunk g is chunk (g % per_row) of row
 // (g / per_row). For fewer than 2^31 chunks the quotient comes from one
@@ -304,7 +305,6 @@ __device__ __forceinline__ void quantise8(const Eight<T>& v, const Eight<T>& u, 
   top = kSwiglu ? abs_max8(h) : abs_max<T>(v);
 #pragma unroll
   for (int o = 1; o < kLanes; o *= 2) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
-  const bool bad = !(top <= 3.402823466e38f);  // infinite or NaN
 
   // largest |h| in 64 bits, for the rare border cases of the scale
   auto top_f64 = [&]() {
@@ -314,32 +314,44 @@ __device__ __forceinline__ void quantise8(const Eight<T>& v, const Eight<T>& u, 
     return t;
   };
 
+  // SwiGLU values next to the end of the fp32 range: the computed one does not
+  // tell whether they are inside, and may be infinite
+  const float held = kSwiglu ? fminf(top, kLargest) : top;
+
   float s, inv;  // block scale without g, and about 1 / (s g)
+  bool bad;      // an infinity or a NaN, or a value out of the range
   if (kNv) {
-    float q = top * inv6g;
+    float q = held * inv6g;
     __nv_fp8_storage_t b = __nv_cvt_float_to_fp8(q * (1.f - kOff), __NV_SATFINITE, __NV_E4M3);
-    const bool near = !bad && b != __nv_cvt_float_to_fp8(q * (1.f + kOff), __NV_SATFINITE, __NV_E4M3);
-    if (__any_sync(0xffffffffu, near)) {
+    const bool near = b != __nv_cvt_float_to_fp8(q * (1.f + kOff), __NV_SATFINITE, __NV_E4M3);
+    const bool end = kSwiglu && top > kLargest * (1.f - kOff);
+    if (__any_sync(0xffffffffu, near || end)) {
       const double t = top_f64();
       if (near) {
         const float border = border_of(q, 4);  // borders between E4M3 values have 4 mantissa bits
         q = beside(border, t - double(border) * 6.0 * double(g));
         b = __nv_cvt_float_to_fp8(q, __NV_SATFINITE, __NV_E4M3);
       }
+      if (end) top = t <= double(kLargest) ? held : kInf;
     }
+    bad = !(top <= kLargest);
     *scale = bad ? 0x7fu : b;
     s = f16_to_f32(__nv_cvt_fp8_to_halfraw(b, __NV_E4M3).x);
     inv = s > 0.f ? rcp_approx(s * g) : 0.f;
   } else {
     if (kSwiglu) {
-      // the exponent changes at a power of two; the lowest that changes the scale byte (0 to 1) is 2^-124
-      const uint32_t above = __float_as_uint(top * (1.f + kOff)) & 0xff800000u;
-      const bool near = !bad && __float_as_uint(top * (1.f - kOff)) < above && top > 0x1p-125f;
+      // the exponent changes at a power of two, infinity (the end of the range) among them;
+      // the lowest that changes the scale byte (0 to 1) is 2^-124
+      const uint32_t above = __float_as_uint(held * (1.f + kOff)) & 0xff800000u;
+      const bool near = __float_as_uint(held * (1.f - kOff)) < above && held > 0x1p-125f;
       if (__any_sync(0xffffffffu, near)) {
         const double t = top_f64();
-        if (near) top = t < double(__uint_as_float(above)) ? __uint_as_float(above - 1) : __uint_as_float(above);
+        const float border = __uint_as_float(above);
+        if (near && top == top)  // a NaN stays
+          top = (border == kInf ? t <= double(kLargest) : t < double(border)) ? __uint_as_float(above - 1) : border;
       }
     }
+    bad = !(top <= kLargest);
     const int e = max(int(__float_as_uint(top) >> 23) - 2, 0);  // biased floor(log2), less E2M1's largest exponent
     *scale = bad ? 0xffu : uint32_t(e);
     s = e ? __uint_as_float(uint32_t(e) << 23) : 0x1p-127f;

@@ -341,8 +341,8 @@ int32_t moe_mxfp_scale_stride(int32_t cols, int32_t format);
  * MX: b - 127 = floor(log2(amax)) - 2, at least -127. NV: s = amax / (6 g)
  * rounded to E4M3 (nearest even, at most 448). Elements: x over the scale,
  * rounded to E2M1 (nearest even, at most 6), decided on the exact quotient. A
- * block holding an infinity or a NaN (or whose silu(gate) * up leaves the
- * fp32 range) gets a NaN scale and codes 0.
+ * block holding an infinity or a NaN (or a silu(gate) * up beyond the largest
+ * fp32 number) gets a NaN scale and codes 0.
  */
 #define MOE_FP_SWIGLU 1u
 moe_status moe_mxfp_quantize(const void* x, int32_t dtype, int64_t rows, int32_t cols, int32_t format,

@@ -1,11 +1,14 @@
 """SwiGLU quantisation at the ends of the fp32 range, byte for byte against
-fp64."""
+fp64: where a scale's border or an intermediate product lies next to or below
+the smallest normal number, and where the values end."""
 import pytest
 import torch
 
 from tests import mxfp_reference as ref
 
 pytestmark = pytest.mark.gpu
+
+FMAX = 2.0 ** 128 - 2.0 ** 104  # the largest fp32 number
 
 
 def _check(gate, up, fmt, g=None):
@@ -17,6 +20,7 @@ def _check(gate, up, fmt, g=None):
     scales = torch.zeros(rows, L.mxfp_scale_stride(cols, fmt), dtype=torch.uint8, device="cuda")
     L.mxfp_quantize(x, codes, scales, fmt, None if g is None else torch.tensor([g], device="cuda"), swiglu=True)
     v = ref.swiglu(x)
+    v = torch.where(v.abs() > FMAX, float("inf"), v)  # not held in fp32: the block becomes NaN
     code, byte = ref.quantise(v, fmt, 1.0 if g is None else float(torch.tensor(g)))
     torch.testing.assert_close(scales, ref.pad_scales(byte, cols, fmt), rtol=0, atol=0)
     torch.testing.assert_close(codes, ref.pack(code), rtol=0, atol=0)
@@ -61,3 +65,23 @@ def test_gates_below_the_normal_range(fmt, g):
     code, byte = _check(gate, up, fmt, g)
     if fmt == "mx":
         assert code[0, :2].tolist() == [2, 6]
+
+
+@pytest.mark.parametrize("fmt,g", [("mx", None), ("nv", None), ("nv", 2.0 ** 88)])
+def test_values_beside_the_end_of_the_range(fmt, g):
+    """Just below the largest fp32 number and just above: a block is NaN from there on."""
+    r = torch.Generator().manual_seed(3)
+    gate = 60 * torch.rand(400, 32, generator=r) + 1
+    silu = gate.double() / (1 + torch.exp(-gate.double()))
+    step = torch.randint(-3, 4, (400, 1), generator=r).double()
+    up = (FMAX / silu * (1 + step * 2.0 ** -24)).float()
+    few = torch.rand(400, 32, generator=r) < 0.9  # the rest of a block well inside
+    up = torch.where(few, up / 8, up)
+    nan = 255 if fmt == "mx" else 0x7F
+    code, byte = _check(gate, up, fmt, g)
+    assert (byte == nan).any() and (byte != nan).any()
+    # infinities and NaN next to values at the end, in either half
+    for half, v in ((0, float("inf")), (1, float("nan")), (1, float("-inf"))):
+        halves = [gate.clone(), up.clone()]
+        halves[half][::3, 5] = v
+        _check(*halves, fmt, g)
