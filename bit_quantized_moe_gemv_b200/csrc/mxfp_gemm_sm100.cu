@@ -107,6 +107,22 @@ struct alignas(16) Tile {
   int e, m0, row0, rows;
 };
 
+// ga gb as the product of two factors that are each in the normal range, and
+// with which no product on the way to the result leaves it before the result
+// does: 2^-180 to 2^180 is more than fp32 holds, while the sums, 2^-20 to 2^47
+// in size, take most of it back.
+struct Factors {
+  float first, second;
+};
+__device__ __forceinline__ Factors factors(float ga, float gb) {
+  const float p = ga * gb;
+  if (p >= 0x1p-90f && p <= 0x1p90f) return {p, 1.f};
+  int ea, eb;
+  const float m = frexpf(ga, &ea) * frexpf(gb, &eb);
+  const int half = (ea + eb) / 2;
+  return {ldexpf(m, half), ldexpf(1.f, ea + eb - half)};
+}
+
 // Token tiles of an expert with `rows` rows.
 __device__ __forceinline__ int token_tiles(int rows, int tn) { return (rows + tn - 1) / tn; }
 
@@ -551,7 +567,8 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
       const float ga = a.a_tscale ? *a.a_tscale : 1.f;
       for (int i = 0; i < n; ++i, ++it) {
         const Tile ti = list_sh[i];
-        const float alpha = a.b_tscale ? ga * a.b_tscale[ti.e] : ga;
+        const Factors f = kNv ? factors(ga, a.b_tscale ? a.b_tscale[ti.e] : 1.f) : Factors{1.f, 1.f};
+        auto scaled = [&](uint32_t sum) { return from_f32<OT>(__uint_as_float(sum) * f.first * f.second); };
         const int n0 = ti.m0 + 32 * q;
         if (!warp_wait_sleep(accf_bar[it & 1], uint32_t(it >> 1) & 1u)) {
           fail(7000005);
@@ -569,7 +586,7 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
           if (a.vec_store) {
             OT* sc = reinterpret_cast<OT*>(scratch);
 #pragma unroll
-            for (int j = 0; j < kTok; ++j) sc[j * 32 + lane] = from_f32<OT>(__uint_as_float(v[j]) * alpha);
+            for (int j = 0; j < kTok; ++j) sc[j * 32 + lane] = scaled(v[j]);
             __syncwarp();
             OT* o = out + (size_t)(ti.row0 + c0 + lane / kPieces) * a.N + n0 + lane % kPieces * kPerPiece;
             const bool in = n0 + lane % kPieces * kPerPiece < a.N;
@@ -585,7 +602,7 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
             OT* o = out + (size_t)(ti.row0 + c0) * a.N + n0 + lane;
 #pragma unroll
             for (int j = 0; j < kTok; ++j)
-              if (c0 + j < ti.rows) o[(size_t)j * a.N] = from_f32<OT>(__uint_as_float(v[j]) * alpha);
+              if (c0 + j < ti.rows) o[(size_t)j * a.N] = scaled(v[j]);
           }
         }
         ptx::tc_fence_before();

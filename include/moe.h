@@ -368,7 +368,9 @@ moe_status moe_mxfp_dequantize(const uint8_t* codes, const uint8_t* scales, int6
  * 0 <= R <= 2^30, 1 <= E <= 1024, 1 <= N <= 2^24, R N <= 2^40, K a multiple of 32
  * up to 2^24, N K < 2^41. A wait inside the kernel that runs out flags
  * MOE_ERR_TIMEOUT; `out` is then undefined.
- * Sums are fp32 on the fp4 tensor cores, rounded once. A NaN scale makes every
+ * Sums are fp32 on the fp4 tensor cores. ga gb[e] multiplies them in fp32 (two
+ * roundings; their product may leave the fp32 range where the result does not),
+ * then comes the one rounding to `out_dtype`. A NaN scale makes every
  * result of its row (or of its weight row's column) NaN.
  */
 moe_status moe_mxfp_matmul(const uint8_t* a_codes, const uint8_t* a_scales, const float* a_tensor_scale, int32_t R,
