@@ -758,11 +758,9 @@ extern "C" moe_status moe_mxfp_matmul(const uint8_t* a_codes, const uint8_t* a_s
       (!narrow_tiles(R, E) && !byte_map(&m.tall, a_codes, K / 2, R, 1, 2, kBKBytes, kWideTN)) ||
       !byte_map(&m.wscales, b_scales, S, N, E, 3, kSlotRow, kBM) ||
       !byte_map(&m.tscales, a_scales, S, R, 1, 2, kSlotRow, kBoxRows))
-    return MOE_ERR_CUDA;
+    return launched(cudaErrorInvalidValue);
   Args a{a_tensor_scale, b_tensor_scale, offsets, out, ws_at<WsHeader>(ws, 0), R, K, N, E,
          int((size_t(N) * size) % 16 == 0 && ptr_aligned(out, 16))};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = format == MOE_FP_NV ? run_out<true>(out_dtype, m, a, st)
-                                            : run_out<false>(out_dtype, m, a, st);
-  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return launched(format == MOE_FP_NV ? run_out<true>(out_dtype, m, a, st) : run_out<false>(out_dtype, m, a, st));
 }

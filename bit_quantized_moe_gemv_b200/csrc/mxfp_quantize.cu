@@ -599,7 +599,7 @@ moe_status moe_mxfp_quantize(const void* x, int32_t dtype, int64_t rows, int32_t
     e = quantize_as<__half>(nv, swiglu, x, rows, cols, tensor_scale, rows_dev, codes, scales, st);
   else
     e = quantize_as<float>(nv, swiglu, x, rows, cols, tensor_scale, rows_dev, codes, scales, st);
-  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return launched(e);
 }
 
 moe_status moe_mxfp_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int32_t cols, int32_t format,
@@ -617,7 +617,7 @@ moe_status moe_mxfp_dequantize(const uint8_t* codes, const uint8_t* scales, int6
     e = dequantize_as<__half>(nv, codes, scales, rows, cols, tensor_scale, rows_dev, out, st);
   else
     e = dequantize_as<float>(nv, codes, scales, rows, cols, tensor_scale, rows_dev, out, st);
-  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return launched(e);
 }
 
 }  // extern "C"

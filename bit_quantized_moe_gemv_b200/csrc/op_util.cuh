@@ -24,6 +24,14 @@ inline moe_status status_ws_check(const void* ws, size_t ws_bytes) {
   return ws_bytes < size_t(MOE_STATUS_BYTES) ? MOE_ERR_WORKSPACE_TOO_SMALL : MOE_OK;
 }
 
+// The status of a call that ends with `e`. A failure also stays behind as the
+// runtime's last error, which the next launch of another call would report as its own.
+inline moe_status launched(cudaError_t e) {
+  if (e == cudaSuccess) return MOE_OK;
+  cudaGetLastError();
+  return MOE_ERR_CUDA;
+}
+
 // Bytes of one element, 0 for an unknown type.
 inline int dtype_size(int32_t dtype) {
   switch (dtype) {

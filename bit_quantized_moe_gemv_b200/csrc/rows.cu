@@ -344,8 +344,6 @@ moe_status rows_check(const void* a, const void* b, int32_t dtype, bool bytes_ok
   return status_ws_check(ws, ws_bytes);
 }
 
-moe_status launched(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
-
 }  // namespace
 }  // namespace moe
 
