@@ -1,5 +1,6 @@
-"""Build the in-tree CUDA library libmoe_b200.so for sm_100a with nvcc, and the
-fast path of its Python binding (_native.so) with g++ against torch's headers.
+"""Build the in-tree CUDA library libmoe_b200.so for sm_100a with nvcc and, where
+torch is installed, the fast path of its Python binding (_native.so) with g++
+against torch's headers. The library itself has no need of torch.
 
     python -m bit_quantized_moe_gemv_b200.build [--force]
 """
@@ -51,14 +52,20 @@ def up_to_date() -> bool:
     return _newer(LIB, _deps())
 
 
-def build_native(force: bool = False) -> str:
-    """The binding's fast path: a CPython module over torch's C++ tensors."""
+def build_native(force: bool = False) -> str | None:
+    """The binding's fast path: a CPython module over torch's C++ tensors. None
+    without torch, which the binding needs as well."""
     src = os.path.join(CSRC, "binding.cpp")
     if not force and _newer(NATIVE, [src, os.path.join(INCLUDE, "moe.h")]):
         return NATIVE
     import sysconfig
 
-    import torch
+    try:
+        import torch
+    except ModuleNotFoundError as e:
+        if e.name != "torch":
+            raise
+        return None
     t = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
     tmp = NATIVE + ".tmp"
@@ -96,13 +103,13 @@ def build(force: bool = False, verbose: bool = False) -> str:
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
         native = ex.submit(build_native, force)
         objs = list(ex.map(compile_one, sources()))
-        native.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc, "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    native.result()  # whatever became of the fast path, the library is there
     return LIB
 
 
