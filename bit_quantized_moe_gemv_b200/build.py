@@ -52,11 +52,28 @@ def up_to_date() -> bool:
     return _newer(LIB, _deps())
 
 
+def _made_for() -> str:
+    """The torch and the interpreter whose headers the fast path is compiled
+    against, or an empty text without torch. Held in the file itself."""
+    from importlib import metadata
+    try:
+        return f"made for torch {metadata.version('torch')}, {sys.implementation.cache_tag}"
+    except metadata.PackageNotFoundError:
+        return ""
+
+
+def _native_up_to_date() -> bool:
+    if not _newer(NATIVE, [os.path.join(CSRC, "binding.cpp"), os.path.join(INCLUDE, "moe.h")]):
+        return False
+    with open(NATIVE, "rb") as f:
+        return _made_for().encode() in f.read()
+
+
 def build_native(force: bool = False) -> str | None:
     """The binding's fast path: a CPython module over torch's C++ tensors. None
     without torch, which the binding needs as well."""
     src = os.path.join(CSRC, "binding.cpp")
-    if not force and _newer(NATIVE, [src, os.path.join(INCLUDE, "moe.h")]):
+    if not force and _native_up_to_date():
         return NATIVE
     import sysconfig
 
@@ -70,7 +87,8 @@ def build_native(force: bool = False) -> str | None:
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
     tmp = NATIVE + ".tmp"
     cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DMOE_MADE_FOR="{_made_for()}"',
+           "-I", INCLUDE,
            "-isystem", os.path.join(t, "include"),
            "-isystem", os.path.join(t, "include", "torch", "csrc", "api", "include"),
            "-isystem", os.path.join(cuda, "include"), "-isystem", sysconfig.get_paths()["include"], src, "-o", tmp,

@@ -260,7 +260,11 @@ PyMethodDef methods[] = {
     MOE_FAST("matmul", matmul, 10),
     {nullptr, nullptr, 0, nullptr},
 };
-PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+#ifndef MOE_MADE_FOR
+#define MOE_MADE_FOR ""
+#endif
+// The doc text says which torch and Python this was compiled for; the build looks for it.
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", MOE_MADE_FOR, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
 
