@@ -298,16 +298,20 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
     *abort_p = 1;
   };
   // One lane polls, the warp follows and agrees on the outcome, so that no
-  // lane leaves a loop alone when a wait gives up.
+  // lane leaves a loop alone when a wait gives up. A vote orders no memory: every
+  // lane then looks at the completed phase itself, which is what shows it the data.
+  auto follow = [&](bool got, uint32_t bar, uint32_t parity) {
+    const bool all = __all_sync(0xffffffffu, got) != 0;
+    ptx::mbar_test_wait(bar, parity);
+    return all;
+  };
   auto warp_wait = [&](uint64_t& bar, uint32_t parity) {
-    bool got = true;
-    if (lane == 0) got = ptx::mbar_wait(ptx::smem_addr(&bar), parity, abort_p);
-    return __all_sync(0xffffffffu, got) != 0;
+    const uint32_t at = ptx::smem_addr(&bar);
+    return follow(lane != 0 || ptx::mbar_wait(at, parity, abort_p), at, parity);
   };
   auto warp_wait_sleep = [&](uint64_t& bar, uint32_t parity) {
-    bool got = true;
-    if (lane == 0) got = ptx::mbar_wait_sleep(ptx::smem_addr(&bar), parity, abort_p, 32);
-    return __all_sync(0xffffffffu, got) != 0;
+    const uint32_t at = ptx::smem_addr(&bar);
+    return follow(lane != 0 || ptx::mbar_wait_sleep(at, parity, abort_p, 32), at, parity);
   };
   auto stage = [&](int s) { return ptx::smem_addr(smem) + uint32_t(s) * C::kStageBytes; };
 
