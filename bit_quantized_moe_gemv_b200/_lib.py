@@ -104,8 +104,8 @@ def launch_count() -> int:
 
 
 def set_wait_cycles(cycles: int) -> int:
-    """Budget of every bounded wait of later fused decode launches (testing
-    the failure path); negative restores the default. Returns the previous."""
+    """Budget of every bounded wait of later fused decode launches and fp4
+    products (testing the failure path); negative restores the default. Returns the previous."""
     return int(LIB.moe_set_wait_cycles(int(cycles)))
 
 

@@ -61,8 +61,8 @@ cudaError_t launch_decode_fused(const uint16_t* x, int T, int H, int I, int E, i
                                 float* sgate_ws, uint32_t* heat, const int32_t* perm_src, const int32_t* offsets,
                                 const int32_t* counts, uint16_t* y_perm, cudaStream_t st);
 constexpr long long kDefaultWaitCycles = 2000000000LL;  // about 1 s at the B200's clock
-// The budget (SM clock cycles) every bounded wait of the fused decode launch
-// gets: kDefaultWaitCycles unless moe_set_wait_cycles changed it.
+// The budget (SM clock cycles) every bounded wait of the fused decode launch and
+// of the fp4 product gets: kDefaultWaitCycles unless moe_set_wait_cycles changed it.
 long long wait_cycles();
 
 // Prefill experts on tcgen05 (expert_gemm_sm100.cu): plan, gather, gate/up

@@ -96,6 +96,7 @@ struct Args {
   WsHeader* hdr;
   int R, K, N, E;
   int vec_store;           // rows of out are 16-byte aligned
+  long long wait_cycles;   // budget of every wait of the pipeline
 };
 
 // Tensor maps: codes and scales of the weights and of the tokens.
@@ -138,6 +139,7 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
   __shared__ __align__(8) uint64_t accf_bar[2], acce_bar[2], drain_bar;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh;
+  __shared__ uint32_t sent_sh[2];        // stages that the weights' and the tokens' warp have copied (mod 2^32)
   constexpr int kExperts = C::kNarrow ? 1 : kMaxE + 1;
   __shared__ int off_sh[kExperts];       // first row of each expert
   __shared__ int first_sh[2][kExperts];  // its first token tile among experts with one, with several
@@ -164,6 +166,7 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
     }
     ptx::mbar_init(ptx::smem_addr(&drain_bar), 1);
     abort_sh = 0;
+    sent_sh[0] = sent_sh[1] = 0;
     ptx::mbar_init_fence();
   } else if (warp == 1) {
     ptx::tmem_alloc(ptx::smem_addr(&tmem_base_sh), C::kTmemCols);
@@ -297,6 +300,7 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
     flag_error(a.hdr, MOE_ERR_TIMEOUT, where);
     *abort_p = 1;
   };
+  auto wait = [&](uint32_t bar, uint32_t parity) { return ptx::mbar_wait(bar, parity, abort_p, a.wait_cycles); };
   // One lane polls, the warp follows and agrees on the outcome, so that no
   // lane leaves a loop alone when a wait gives up. A vote orders no memory: every
   // lane then looks at the completed phase itself, which is what shows it the data.
@@ -307,11 +311,11 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
   };
   auto warp_wait = [&](uint64_t& bar, uint32_t parity) {
     const uint32_t at = ptx::smem_addr(&bar);
-    return follow(lane != 0 || ptx::mbar_wait(at, parity, abort_p), at, parity);
+    return follow(lane != 0 || wait(at, parity), at, parity);
   };
   auto warp_wait_sleep = [&](uint64_t& bar, uint32_t parity) {
     const uint32_t at = ptx::smem_addr(&bar);
-    return follow(lane != 0 || ptx::mbar_wait_sleep(at, parity, abort_p, 32), at, parity);
+    return follow(lane != 0 || ptx::mbar_wait_sleep(at, parity, abort_p, 32, a.wait_cycles), at, parity);
   };
   auto stage = [&](int s) { return ptx::smem_addr(smem) + uint32_t(s) * C::kStageBytes; };
 
@@ -333,6 +337,7 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
       // A copy takes its thread about 70 cycles, hence two threads and, for a
       // token tile that is nearly full, one copy.
       bool ready = false;
+      sent_sh[warp != 0] = uint32_t(first_tile + n) * uint32_t(KB);
       for (int i = 0; i < n; ++i) {
         const Tile ti = list_sh[i];
         const bool whole = !C::kNarrow && ti.rows > kTN - kBoxRows;
@@ -341,7 +346,7 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
         const CUtensorMap* tmap = whole ? &maps.tall : &maps.tcodes;
         int kb = 0;
         for (; kb < KB; ++kb) {
-          if (!ready && !ptx::mbar_wait(ptx::smem_addr(&empty_bar[s]), ph ^ 1u, abort_p)) break;
+          if (!ready && !wait(ptx::smem_addr(&empty_bar[s]), ph ^ 1u)) break;
           const uint32_t bar = ptx::smem_addr(&full_bar[s]), dst = stage(s);
           ptx::mbar_arrive_expect_tx(bar, bytes);
           if (warp == 0)
@@ -358,6 +363,7 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
           ready = ptx::mbar_test_wait(ptx::smem_addr(&empty_bar[s]), ph ^ 1u);
         }
         if (kb < KB) {
+          sent_sh[warp != 0] = uint32_t(first_tile + i) * uint32_t(KB) + uint32_t(kb);
           fail(7000001);
           break;
         }
@@ -385,7 +391,7 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
         // One stage: descriptors count in 16 bytes. `second`: MX, the other
         // half of the scale words that the stage before copied.
         auto step = [&](bool second, uint64_t dsc, int steps) {
-          if (!ready && !ptx::mbar_wait(full0 + 8 * s, ph, abort_p)) return false;
+          if (!ready && !wait(full0 + 8 * s, ph)) return false;
           ptx::tc_fence_after();
           if (!second) {
 #pragma unroll
@@ -430,11 +436,11 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
           }
           sready = ptx::mbar_test_wait(ptx::smem_addr(&sblock_bar[ss]), sph);
         };
-        auto slot_ready = [&]() { return sready || ptx::mbar_wait(ptx::smem_addr(&sblock_bar[ss]), sph, abort_p); };
-        bool good = ptx::mbar_wait(ptx::smem_addr(&acce_bar[it & 1]), (uint32_t(it >> 1) & 1u) ^ 1u, abort_p);
+        auto slot_ready = [&]() { return sready || wait(ptx::smem_addr(&sblock_bar[ss]), sph); };
+        bool good = wait(ptx::smem_addr(&acce_bar[it & 1]), (uint32_t(it >> 1) & 1u) ^ 1u);
         constexpr int kPerSlot = kNv ? 2 : 4;  // stages whose scales a slot holds
         int kb = 0;
-        for (; kb + kPerSlot <= full_stages && good; kb += kPerSlot) {
+        for (; good && kb + kPerSlot <= full_stages; kb += kPerSlot) {
           good = slot_ready();
           if (kNv) {
             good = good && step(false, ds, 4);
@@ -445,6 +451,7 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
             next_buffer();
             good = good && step(false, ds + 128, 4) && step(true, ds + 128, 4);
           }
+          if (!good) break;  // a slot that was not waited for is not given back
           next_buffer();
           next_slot();
         }
@@ -457,7 +464,7 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
             good = step(second, ds + ((kNv ? j : j >> 1) & 1) * 128, kb < full_stages ? 4 : tail_steps);
             if (kNv || second || kb + 1 == KB) next_buffer();
           }
-          next_slot();
+          if (good) next_slot();
         }
         if (!good) {
           fail(7000002);
@@ -473,7 +480,7 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
         const uint32_t bytes = uint32_t((kBM + boxes * kBoxRows) * kSlotRow);
         int x = 0;
         for (; x < stride; x += kSlotRow) {
-          if (!ptx::mbar_wait(ptx::smem_addr(&sempty_bar[ss]), sph ^ 1u, abort_p)) break;
+          if (!wait(ptx::smem_addr(&sempty_bar[ss]), sph ^ 1u)) break;
           const uint32_t bar = ptx::smem_addr(&sfull_bar[ss]);
           const uint32_t dst = ptx::smem_addr(smem) + C::kScaleAt + ss * C::kSlotBytes;
           ptx::mbar_arrive_expect_tx(bar, bytes);
@@ -628,11 +635,25 @@ fp4_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
     if (*abort_p) break;
   }
 
-  // no copy and no MMA may be in flight when the CTA leaves
+  // No copy and no MMA may be in flight when the CTA leaves. They end by
+  // themselves, also after a wait that gave up, so that these waits are met; were
+  // one not within its limit of a second, the CTA would leave all the same.
   if (warp == 1 && ptx::elect_one()) {
     ptx::mma_commit(ptx::smem_addr(&drain_bar));
     ptx::mbar_wait(ptx::smem_addr(&drain_bar), 0, nullptr);
-  } else if (warp == 0 || warp == 3) {  // a stage is full when both warps' copies are there
+  } else if (warp == 0 || warp == 3) {
+    // A stage is full when both warps' copies are there. After a wait that gave
+    // up one of them may have stopped earlier: it arrives without a copy (it is at
+    // most a ring behind, and where it stopped the stage waits for it alone).
+    for (uint32_t i = sent_sh[warp != 0]; int(sent_sh[warp == 0] - i) > 0; ++i) {
+      if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&full_bar[s]));
+      issued = min(issued + 1, kStages);
+      if (++s == kStages) {
+        s = 0;
+        ph ^= 1u;
+      }
+    }
+    __syncwarp();
     for (int i = 0; i < issued; ++i) {
       if (--s < 0) {
         s = kStages - 1;
@@ -764,7 +785,7 @@ extern "C" moe_status moe_mxfp_matmul(const uint8_t* a_codes, const uint8_t* a_s
       !byte_map(&m.tscales, a_scales, S, R, 1, 2, kSlotRow, kBoxRows))
     return launched(cudaErrorInvalidValue);
   Args a{a_tensor_scale, b_tensor_scale, offsets, out, ws_at<WsHeader>(ws, 0), R, K, N, E,
-         int((size_t(N) * size) % 16 == 0 && ptr_aligned(out, 16))};
+         int((size_t(N) * size) % 16 == 0 && ptr_aligned(out, 16)), wait_cycles()};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return launched(format == MOE_FP_NV ? run_out<true>(out_dtype, m, a, st) : run_out<false>(out_dtype, m, a, st));
 }

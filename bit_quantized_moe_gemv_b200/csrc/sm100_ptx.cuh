@@ -59,14 +59,15 @@ __device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
 // Bounded wait; also gives up early when *abort becomes non-zero. Spins on
 // test_wait: a suspended try_wait resumed the warp too late to keep a
 // pipeline fed.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const volatile int* abort) {
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const volatile int* abort,
+                                          long long cycles = kWaitCycles) {
   if (mbar_test_wait(bar, parity)) return true;
   const long long t0 = clock64();
   for (uint32_t it = 1;; ++it) {
     if (mbar_test_wait(bar, parity)) return true;
     if ((it & 63) == 0) {
       if (abort && *abort) return false;
-      if (clock64() - t0 > kWaitCycles) return false;
+      if (clock64() - t0 > cycles) return false;
     }
   }
 }
@@ -75,7 +76,7 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const v
 // wake-up latency the pipeline hides, so that the waiting warp neither
 // takes issue slots nor shared-memory bandwidth from the warps doing work.
 __device__ __forceinline__ bool mbar_wait_sleep(uint32_t bar, uint32_t parity, const volatile int* abort,
-                                                uint32_t ns) {
+                                                uint32_t ns, long long cycles = kWaitCycles) {
   if (mbar_test_wait(bar, parity)) return true;
   const long long t0 = clock64();
   for (uint32_t it = 1;; ++it) {
@@ -83,7 +84,7 @@ __device__ __forceinline__ bool mbar_wait_sleep(uint32_t bar, uint32_t parity, c
     if (mbar_test_wait(bar, parity)) return true;
     if ((it & 15) == 0) {
       if (abort && *abort) return false;
-      if (clock64() - t0 > kWaitCycles) return false;
+      if (clock64() - t0 > cycles) return false;
     }
   }
 }
