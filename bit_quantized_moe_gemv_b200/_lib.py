@@ -393,6 +393,8 @@ def _rows_of(t, name, bytes_ok=False):
 
 def _pairs(inv_perm, T, dev):
     """(address, k) of an inv_perm [T*k] (or [T, k])."""
+    if inv_perm is None:
+        raise ValueError("inv_perm: required (the call takes no NULL here)")
     n = inv_perm.numel()
     if n % T or n == 0:
         raise ValueError(f"inv_perm: {n} pairs for {T} tokens")

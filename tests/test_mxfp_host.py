@@ -213,3 +213,14 @@ def test_the_fast_path_leaves_everything_doubtful_to_the_checks(L):
     with pytest.raises(ImportError):
         f.bind("/nowhere/libmoe_b200.so")
     f.bind(L._build.LIB)
+
+
+def test_a_missing_inv_perm_is_named(L, rec):
+    ws, w = _u8(8704), torch.zeros(4, 3)
+    for f in (lambda: L.permute(_bf(4, 64), None, _bf(12, 64), ws, stream=0),
+              lambda: L.permute_grad(_bf(12, 64), None, _bf(4, 64), ws, stream=0),
+              lambda: L.unpermute(_bf(12, 64), None, w, _bf(4, 64), ws, stream=0),
+              lambda: L.unpermute_grad(_bf(4, 64), _bf(12, 64), None, w, _bf(12, 64), torch.zeros(4, 3), ws, stream=0)):
+        with pytest.raises(ValueError, match="inv_perm: required"):
+            f()
+    assert rec.calls == []
