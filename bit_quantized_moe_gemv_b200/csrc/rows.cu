@@ -35,8 +35,11 @@ __device__ __forceinline__ int pair_row(const int* inv, long long p, long long n
 // The sums take them as they are, so that no warp is without one however many a
 // row has (8,192 tokens x 1,032 16-bit values, five segments: unpermute 28 us;
 // with eight warps per row 35). permute, which waits for nothing but its own
-// stores, rounds them up to a power of two and lets the surplus warps leave
-// (1,021 tokens x 1,032: 4.2 us, as they are 4.7; no difference at 8,192).
+// stores, rounds them up to a power of two and lets the surplus warps leave, as
+// long as those are at most two for three that stay: five segments in eight warps
+// take 4.3 us at 1,021 tokens x 1,032 (as they are 4.7; the same at 8,192), but
+// nine in sixteen 34.6 us at 8,192 x 1,028 and 6.9 at 1,021 x 2,056 (as they are
+// 24.7 and 6.0).
 struct Segments {
   int per_row, shift;  // shift: log2(per_row) or -1
   long long all;
@@ -46,7 +49,7 @@ Segments row_segments(long long T, int nvec, int seg, bool rounded) {
   const int n = (nvec + seg - 1) / seg;
   int l = 0;
   while ((1 << l) < n) ++l;
-  const int per_row = rounded ? 1 << l : n;
+  const int per_row = rounded && 3LL << l <= 5LL * n ? 1 << l : n;
   return {per_row, per_row == 1 << l ? l : -1, T * per_row};
 }
 // This warp's token and segment; false if there is none.

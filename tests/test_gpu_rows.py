@@ -273,3 +273,19 @@ def test_rows_of_every_number_of_segments(H, dtype):
     ref, mag = terms.sum(1), terms.abs().sum(1)
     assert ((out.double() - ref).abs() <= _half(dtype, ref) * (1 + 2.0 ** -10) + (k + 1) * U * mag).all()
     assert L.get_status(ws) == 0
+
+
+@pytest.mark.parametrize("dtype", DTYPES + [torch.uint8])
+@pytest.mark.parametrize("H", [1028, 2056, 2568, 4104])
+def test_permute_with_and_without_surplus_warps(H, dtype):
+    """Numbers of segments that are rounded up to a power of two, and that are too far from one."""
+    from bit_quantized_moe_gemv_b200 import _lib as L
+    T, k, E = 203, 3, 16
+    _, inv, ws = _routing(T, k, E, H, 0.2)
+    x = (torch.randint(0, 256, (T, H), dtype=torch.uint8).cuda() if dtype == torch.uint8
+         else _rand(T, H, dtype=dtype, seed=1))
+    xp = torch.full((T * k, H), 7, dtype=dtype, device="cuda")
+    want, p = xp.clone(), torch.nonzero(inv >= 0).reshape(-1)
+    want[inv[p].long()] = x[p // k]
+    L.permute(x, inv, xp, ws)
+    assert torch.equal(xp, want) and L.get_status(ws) == 0
