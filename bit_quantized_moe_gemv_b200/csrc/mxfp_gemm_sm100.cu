@@ -24,7 +24,8 @@
 // those stores and the MMAs get in each other's way: 8192^3 MX in 326 us, in
 // 295 with tcgen05.cp. One thread that waits, copies and multiplies is the next
 // limit, then the threads that issue the TMA copies (about 70 cycles each):
-// 238 us now (MX; NV 256), of which the MMAs alone take 141.
+// 251 us now (MX; NV 276; back to back, under the power limit, 292 and 322), of
+// which the MMAs alone take 141.
 //
 // Tiles: every CTA sums up the experts' token tiles (offsets are on the
 // device) and takes tiles b, b + grid, ... of the list "token tile, 128 weight
@@ -38,12 +39,13 @@
 // a tile.
 //
 // Bound: HBM where an expert has up to about 160 rows (512 experts of 160 rows,
-// gate and up: 193 us, 96 % of the measured copy rate; of 16 rows: 154 us), the
+// gate and up: 189 us, 98 % of the measured copy rate; of 16 rows: 135 us), the
 // operands' way beyond (a stage of 160 tokens brings 36 KB from L2 at 64 bytes a
 // cycle and takes 72 KB through shared memory at 128: 576 cycles either way, of
-// 628 measured at 8192^3, where its MMAs take 372), the start of a CTA (barriers,
-// list, first copies: about 3 us) for a token's ten experts (9.1 us, 2.6 us of
-// them HBM time).
+// 670 measured at 8192^3, where its MMAs take 372), the start of a CTA (barriers,
+// list, first copies: about 3 us) for a token's ten experts (9.2 us, 2.6 us of
+// them HBM time), and the few CTAs at work for few rows of one matrix (32 of them
+// for 8 x 4,096 x 4,096: 9.7 us, 1.4 us of HBM time; K is not split).
 #include <cuda.h>
 
 #include <atomic>
@@ -710,7 +712,13 @@ bool byte_map(CUtensorMap* map, const uint8_t* base, uint64_t row_bytes, uint64_
 }
 
 // Tokens per tile. Few rows per expert (at most 32 on average): narrow tiles,
-// two CTAs per SM, so that one's weights stream while the other computes.
+// two CTAs per SM, so that one's weights stream while the other computes. The host
+// knows the average alone. 512 experts, 1,536 x 2,048 MX, cold, narrow and wide:
+// evenly 40 rows 25 and 27 us, 640: 145 and 154, 8,192: 152 and 158, 16,384: 154
+// and 160, 32,768: 180 and 168; skewed (Zipf, an expert at most once a token)
+// 640: 82 and 84, 8,192: 156 and 160, 16,384: 174 and 166, 32,768: 221 and 182. All
+// rows with one expert, which no router of several picks does: 640: 14 and 14,
+// 8,192: 47 and 29, 16,384: 80 and 43.
 constexpr int kNarrowTN = 32, kWideTN = 160;
 bool narrow_tiles(int R, int E) { return R <= 32LL * E; }
 

@@ -16,15 +16,19 @@
 //
 // 8 elements per thread by 16-byte loads, a block's 4 (MX) or 2 (NV) lanes
 // exchange their maxima by shuffles, codes leave as one 32-bit word per thread.
-// Dequantising is bound by HBM (63 M values to bf16: 26 us, 6.1 TB/s).
+// Dequantising is bound by HBM (63 M values to bf16: 26 us in MX, 6.1 TB/s, 27 in NV).
 // Quantising comes close to it where instructions are saved: products and sums
 // two at a time, maxima three at a time, offsets that are constants (lanes side
 // by side on a row), small blocks at 56 registers, 36 warps per SM (of 64
-// registers, 32 warps: 54 us instead of 52). 63 M SwiGLU values of bf16 halves
-// take 52 us (85 % of the copy rate; 22 instructions per value, two of them
-// MUFU), 17 M bf16 values to NV 9.5 us (70 %; 13 instructions, and a fifth of
+// registers, 32 warps: 51 us instead of 50). 63 M SwiGLU values of bf16 halves
+// take 50 us (88 % of the copy rate; 22 instructions per value, two of them
+// MUFU), 17 M bf16 values to NV 10.6 us (63 %; 13 instructions, and a fifth of
 // the time is the start of the grid). Both issue on 0.6 to 0.7 of the
-// cycles with no pipe above two thirds.
+// cycles with no pipe above two thirds. The other forms, at the same two sizes:
+// MX 7.8 us (fp16 7.5, fp32 12.2), NV of fp16 10.4, of fp32 14.3; SwiGLU of fp16
+// 51 us in MX, of bf16 and fp16 57 in NV, of fp32 99 and 105. Those last spill
+// most (up to 180 bytes a thread), and would take 79 and 88 us with 80 registers,
+// where the 16-bit ones take 57 and 62.
 #include <cuda_fp4.h>
 #include <cuda_fp8.h>
 

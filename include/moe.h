@@ -319,9 +319,9 @@ moe_status moe_unpermute_grad(const void* dout, const void* y_perm, int32_t dtyp
  *           multiple of 16 bytes (the product ignores what stands there);
  * with
  *   MOE_FP_MX  blocks of 32, scale byte b is E8M0: 2^(b-127), 255 = NaN;
- *   MOE_FP_NV  blocks of 16, scale byte E4M3, and one fp32 scale per tensor
- *              (NULL = 1) that multiplies all values; it must be a positive
- *              normal number between 2^-90 and 2^90.
+ *   MOE_FP_NV  blocks of 16, scale byte E4M3 with its sign bit 0, 0x7f = NaN, and
+ *              one fp32 scale per tensor (NULL = 1) that multiplies all values;
+ *              it must be a positive normal number between 2^-90 and 2^90.
  * cols is a multiple of 32, at most 2^24, rows * cols at most 2^38; codes, scales
  * and the wide matrix are 16-byte aligned. Outputs overlap no input.
  */
